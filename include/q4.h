@@ -509,10 +509,166 @@ Q4_API q4_status kv_dequant_int4(const uint8_t* packed, const void* scales, int6
                                  int64_t head_dim, int32_t group_size, void* out,
                                  q4_dtype out_dtype, q4_stream stream);
 
+/* ---------------------------------------------------- paged INT8 KV cache
+ *
+ * One layer's INT8 cache as a pool of pages, and the four operators a decode
+ * loop needs of it: the write of new tokens, attention over the cached ones,
+ * the attention weight each of them received, and eviction by that weight.
+ * The rows are those of kv_quantize_int8 ("压缩算法" (cs-knowledge-wiki)
+ * section 7.4.1.1): a pool viewed as rows of head_dim values is what
+ * kv_quantize_int8 writes and kv_dequant_int8 reads.  Which tokens a cache may
+ * drop is the subject of "LLM 后训练量化深度实战" (ybb.press) section 七 (sink
+ * tokens, recent tokens).
+ *
+ * Arrays on the device (lengths, tables, slots) are read by the kernels; what
+ * is out of range in them is brought into range, nothing is read or written
+ * out of bounds, and the next q4_sync_status returns Q4_ERR_INVALID_ARG.
+ */
+typedef struct kv_paged_int8 {
+    int8_t* k_codes;  /* [pages, heads, page_size, head_dim], 16-byte aligned */
+    void* k_scales;   /* [pages, heads, page_size] in the cache type, >= 0 */
+    int8_t* v_codes;
+    void* v_scales;
+    int64_t k_codes_stride;  /* elements from a page to the next, at least a dense page's; */
+    int64_t k_scales_stride; /* the codes' a multiple of 16 */
+    int64_t v_codes_stride;
+    int64_t v_scales_stride;
+    int64_t pages;       /* 1 .. 2^31 - 1 */
+    int32_t heads;       /* KV heads, 1 .. 4096 */
+    int32_t page_size;   /* tokens of a page, 1 .. 2^20 (any; multiples of 16 are fastest) */
+    int32_t head_dim;    /* a multiple of 16 in [16, 256] */
+    q4_dtype dtype;      /* Q4_F16 or Q4_BF16: of the scales, and of q, k, v and outputs */
+} kv_paged_int8;
+
+/* A batch of sequences over a pool. */
+typedef struct kv_batch {
+    const int32_t* block_table; /* [seqs, table_width]: page of each page_size tokens.  Entries
+                                   beyond a sequence's length are not read. */
+    const int32_t* seq_lens;    /* [seqs]: cached tokens of each sequence, the new ones among them */
+    const int32_t* cu_new;      /* [seqs + 1]: rows cu_new[b] .. cu_new[b+1] - 1 of q are sequence
+                                   b's new tokens, its last ones; NULL: row b is sequence b's one
+                                   new token */
+    int64_t table_width;        /* table_width * page_size < 2^31 - 2^16 */
+    int64_t tokens;             /* rows of q; rows that no sequence names are left as they are */
+    int64_t max_new;            /* >= 1: the most new tokens of a sequence.  Only the choice of
+                                   kernel depends on it. */
+    int32_t seqs;
+} kv_batch;
+
+/*
+ * The new tokens of a layer into its cache, in one pass: each query and key
+ * head is normalized (RMS norm over head_dim, fp32; skipped where the weight
+ * is NULL) and rotated by its position; queries are written out, keys and
+ * values quantized into their slots.
+ *   x^ = x / sqrt(mean(x^2) + eps) * w
+ *   phi_i = position * inv_freq[i], i < rot_dim / 2 (the turn reduced in fp64, so far
+ *   positions keep their angle); the pair (x^_a, x^_b) becomes
+ *   (a cos phi - b sin phi, b cos phi + a sin phi), a = i, b = i + rot_dim/2, or
+ *   a = 2i, b = 2i + 1 (interleaved); elements from rot_dim on are not rotated.
+ *   Codes and scale as kv_quantize_int8, from the fp32 rotated key (no
+ *   rounding to 16 bits in between) and from the value as it is.
+ *
+ *   q, k, v    [tokens, q_heads | heads | heads, head_dim] in the cache type, rows
+ *              q_stride, k_stride, v_stride elements apart (a fused projection's
+ *              output can be passed as it is), 16-byte aligned, strides multiples of 8
+ *   slots      int64 [tokens]: page * page_size + offset.  A negative slot is
+ *              padding: its key and value are not written.  No two tokens may
+ *              name one slot (that slot's row would be either's, or a mixture).
+ *   positions  int32 [tokens];  inv_freq  fp32 [rot_dim / 2]
+ *   rot_dim    0 (no rotation) .. head_dim; a multiple of 16, or of 2 if interleaved
+ *   q_norm, k_norm  [head_dim] in the cache type, 16-byte aligned, or NULL
+ *   q_out      [tokens, q_heads, head_dim], rows q_out_stride apart; may be q
+ *              itself (same stride).  q_heads = 0: no queries, q and q_out unused.
+ */
+Q4_API q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_t q_stride,
+                                      int32_t q_heads, const void* k, int64_t k_stride,
+                                      const void* v, int64_t v_stride, int64_t tokens,
+                                      const int64_t* slots, const int32_t* positions,
+                                      const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                      const void* q_norm, const void* k_norm, float eps,
+                                      void* q_out, int64_t q_out_stride, q4_stream stream);
+
+/*
+ * Cached rows by slot: k_out[t, h] = cache_type(q * s) of the key in slots[t],
+ * v_out likewise; both dense [tokens, heads, head_dim], 16-byte aligned.  Rows
+ * of negative slots are left as they are.
+ */
+Q4_API q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t* slots,
+                                      int64_t tokens, void* k_out, void* v_out, q4_stream stream);
+
+/*
+ * Attention of each sequence's n new tokens over its L cached tokens.  New
+ * token i sees the tokens j <= L - n + i, the last `window` of them if
+ * window > 0:
+ *   S_j = scale * (q . k_j),   out = sum_j e^(S_j) v_j / sum_j e^(S_j),
+ *   lse = log sum_j e^(S_j),
+ * k_j, v_j the dequantized rows (q * s, not rounded).  A row that sees nothing
+ * gives zeros and lse = -inf.  q_heads is a multiple of the cache's heads:
+ * query head h reads KV head h / (q_heads / heads).  The softmax is in fp32
+ * with one rounding of the weights to fp16 (2^-11) before the product with V.
+ * V scales below 2^-100 count as 2^-100.  A masked token's row does not reach
+ * the output whatever its scales hold; a visible NaN does.
+ *   q          [tokens, q_heads, head_dim] in the cache type, rows q_stride apart
+ *   out        the same shape, rows out_stride apart; must not overlap q
+ *   lse        fp32 [tokens, q_heads], or NULL
+ *   scale      any finite value
+ *   workspace  kv_attention_workspace_bytes(head_dim, q_heads, heads, max_new)
+ *              bytes, 256-byte aligned, its first 256 KiB zero-filled before the first use (a
+ *              call leaves them so); the INT4 products' workspace serves too if large enough.
+ *              Calls that may overlap on the GPU need separate buffers.
+ * The work is divided on the device by the lengths found there, so the call
+ * can be captured and replayed with other lengths; the result does not depend on
+ * timing.  tokens * q_heads < 2^31 - 2^16.
+ */
+Q4_API size_t kv_attention_workspace_bytes(int32_t head_dim, int32_t q_heads, int32_t kv_heads,
+                                           int64_t max_new);
+Q4_API q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q,
+                                         int64_t q_stride, int32_t q_heads, const kv_batch* batch,
+                                         float scale, int64_t window, void* out,
+                                         int64_t out_stride, float* lse, void* workspace,
+                                         size_t workspace_bytes, q4_stream stream);
+
+/*
+ * The attention weight the cached tokens received from these queries, added to
+ * what earlier calls found: for every sequence, KV head h and token j
+ *   mass[page, h, slot] += sum over the rows of h that see j of e^(S_j - lse).
+ *   lse   fp32 [tokens, q_heads] as kv_attention_int8_paged returned it for the
+ *         same queries, scale and window
+ *   mass  fp32 [pages, heads, page_size], pages mass_stride elements apart
+ * A page that several sequences share gets the sum of theirs (in any order).
+ */
+Q4_API q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q,
+                                              int64_t q_stride, int32_t q_heads, const float* lse,
+                                              const kv_batch* batch, float scale, int64_t window,
+                                              float* mass, int64_t mass_stride, q4_stream stream);
+
+/*
+ * Eviction: each sequence and KV head keeps the first `sinks` tokens, the last
+ * `recent` and, of the others, those of the largest mass (equal masses: the
+ * lower index; a NaN is below all), `budget` in all -- or everything, where it has no more --
+ * and the kept rows of K, V, scales and mass move, in their order, to tokens
+ * 0, 1, ... of the destination pages.  What lies behind them stays as it is.
+ *   batch     block_table, seq_lens, table_width, seqs (the rest is not used)
+ *   budget    >= 1;  recent, sinks >= 0, recent + sinks <= budget
+ *   dst_table [seqs, dst_width] pages that get the kept tokens, none of them a
+ *             page of any sequence here (prefix pages shared with others stay
+ *             whole that way); or NULL or block_table itself: in place, where
+ *             no page may belong to two of the sequences
+ *   new_lens  int32 [seqs] (written): min(length, budget); may be seq_lens
+ *   workspace kv_evict_workspace_bytes(seqs, heads, budget) bytes, 16-byte aligned
+ */
+Q4_API size_t kv_evict_workspace_bytes(int32_t seqs, int32_t heads, int64_t budget);
+Q4_API q4_status kv_evict_int8_paged(const kv_paged_int8* cache, float* mass, int64_t mass_stride,
+                                     const kv_batch* batch, int64_t budget, int64_t recent,
+                                     int64_t sinks, const int32_t* dst_table, int64_t dst_width,
+                                     int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                                     q4_stream stream);
+
 /*
  * Waits for `stream`, then reports the first device-side error recorded
  * since the previous call (Q4_ERR_TIMEOUT when a kernel's bounded wait ran
- * out, Q4_ERR_INVALID_ARG when a permutation entry was out of range) or a
+ * out, Q4_ERR_INVALID_ARG when a permutation entry, a cache slot, a page, a
+ * length or an activation was out of range) or a
  * pending CUDA error (Q4_ERR_CUDA), and clears the record.
  */
 Q4_API q4_status q4_sync_status(q4_stream stream);

@@ -10,7 +10,9 @@ Names follow the C ABI: ``q4_quantize_pack``, ``q4_dequant``, ``q4_gemv``,
 ``q4_gemm_skinny``, ``bf16_gemv_ref_bw``, ``q4_sync_status``, the per-channel
 INT8 weight calls ``q8_quantize_per_channel``, ``q8_dequant``, ``q8_gemv`` and
 the KV-cache calls ``kv_quantize_int8``, ``kv_dequant_int8``,
-``kv_quantize_int4``, ``kv_dequant_int4``.
+``kv_quantize_int4``, ``kv_dequant_int4``, and on a paged INT8 cache
+``kv_append_int8_paged``, ``kv_gather_int8_paged``, ``kv_attention_int8_paged``,
+``kv_attention_mass_int8_paged``, ``kv_evict_int8_paged``.
 """
 from __future__ import annotations
 
@@ -44,6 +46,9 @@ ABI_SYMBOLS = (
     "q8_gemv", "kv_quantize_int8", "kv_dequant_int8", "kv_quantize_int4", "kv_dequant_int4",
     "mxfp4_quantize", "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "q4_gemv_grouped",
     "fp4_gemm_workspace_bytes", "fp4_gemm", "bf16_ref_workspace_bytes",
+    "kv_append_int8_paged", "kv_gather_int8_paged", "kv_attention_workspace_bytes",
+    "kv_attention_int8_paged", "kv_attention_mass_int8_paged", "kv_evict_workspace_bytes",
+    "kv_evict_int8_paged",
 )
 
 
@@ -67,6 +72,36 @@ class _CWeight(ctypes.Structure):
         ("group_size", ctypes.c_int32),
         ("bits", ctypes.c_int32),
         ("symmetric", ctypes.c_int32),
+    ]
+
+
+class _CKVPaged(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("k_codes_stride", ctypes.c_int64),
+        ("k_scales_stride", ctypes.c_int64),
+        ("v_codes_stride", ctypes.c_int64),
+        ("v_scales_stride", ctypes.c_int64),
+        ("pages", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class _CKVBatch(ctypes.Structure):
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p),
+        ("table_width", ctypes.c_int64),
+        ("tokens", ctypes.c_int64),
+        ("max_new", ctypes.c_int64),
+        ("seqs", ctypes.c_int32),
     ]
 
 
@@ -119,13 +154,26 @@ def load_library(path: str = LIB_PATH):
     lib.fp4_gemm_workspace_bytes.argtypes = [I32, I64, I64, I64]
     lib.fp4_gemm_workspace_bytes.restype = ctypes.c_size_t
     lib.fp4_gemm.argtypes = [I32, P, P, P, I64, I64, P, P, P, I64, P, S, P, ctypes.c_size_t, P]
+    KV, KB, F, Z = ctypes.POINTER(_CKVPaged), ctypes.POINTER(_CKVBatch), ctypes.c_float, ctypes.c_size_t
+    lib.kv_append_int8_paged.argtypes = [KV, P, I64, I32, P, I64, P, I64, I64, P, P, P, I32, I32, P,
+                                         P, F, P, I64, P]
+    lib.kv_gather_int8_paged.argtypes = [KV, P, I64, P, P, P]
+    lib.kv_attention_workspace_bytes.argtypes = [I32, I32, I32, I64]
+    lib.kv_attention_workspace_bytes.restype = Z
+    lib.kv_attention_int8_paged.argtypes = [KV, P, I64, I32, KB, F, I64, P, I64, P, P, Z, P]
+    lib.kv_attention_mass_int8_paged.argtypes = [KV, P, I64, I32, P, KB, F, I64, P, I64, P]
+    lib.kv_evict_workspace_bytes.argtypes = [I32, I32, I64]
+    lib.kv_evict_workspace_bytes.restype = Z
+    lib.kv_evict_int8_paged.argtypes = [KV, P, I64, KB, I64, I64, I64, P, I64, P, P, Z, P]
     for f in ("q4_quantize_pack", "q4_quantize_pack_clip", "q4_quantize_pack_perm",
               "q4_permute_activations", "q4_dequant", "q4_gemv",
               "q4_gemm_skinny", "q4_gemv_noalloc",
               "bf16_gemv_ref_bw", "q4_sync_status", "q4_selftest_wait_timeout",
               "q8_quantize_per_channel", "q8_dequant", "q8_gemv", "kv_quantize_int8",
               "kv_dequant_int8", "kv_quantize_int4", "kv_dequant_int4", "mxfp4_quantize",
-              "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "fp4_gemm"):
+              "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "fp4_gemm", "kv_append_int8_paged",
+              "kv_gather_int8_paged", "kv_attention_int8_paged", "kv_attention_mass_int8_paged",
+              "kv_evict_int8_paged"):
         getattr(lib, f).restype = S
     lib.q4_status_string.argtypes = [S]
     lib.q4_status_string.restype = ctypes.c_char_p
@@ -556,6 +604,317 @@ def kv_dequant_int4(packed: torch.Tensor, scales: torch.Tensor, group_size: int 
                              _DT[out.dtype], _stream(stream))
     _check(st, "kv_dequant_int4")
     return out
+
+
+# ------------------------------------------------------ paged INT8 KV cache
+
+@dataclass
+class KVPagedInt8:
+    """One layer's paged INT8 KV cache: codes int8 [pages, heads, page_size,
+    head_dim] and scales [pages, heads, page_size] (fp16 or bf16: the cache
+    type).  Pages may lie apart (a slice of a pool of several layers); inside
+    a page the arrays are dense."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return self.k_scales.dtype
+
+    def c_struct(self) -> _CKVPaged:
+        kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
+        shape = kc.shape
+        if kc.dtype != torch.int8 or vc.dtype != torch.int8 or len(shape) != 4 or vc.shape != shape:
+            raise ValueError("k_codes and v_codes must be int8 [pages, heads, page_size, head_dim]")
+        if ks.dtype not in _DT or vs.dtype != ks.dtype or ks.shape != shape[:3] or vs.shape != shape[:3]:
+            raise ValueError("k_scales and v_scales must be [pages, heads, page_size] of one 16-bit type")
+        pages, heads, ps, d = shape
+        strides = []
+        for x, inner in ((kc, (ps * d, d, 1)), (ks, (ps, 1)), (vc, (ps * d, d, 1)), (vs, (ps, 1))):
+            st = x.stride()
+            if not _dense(x.shape[1:], st[1:], inner):
+                raise ValueError("a page's codes and scales must be dense")
+            strides.append(st[0] if pages > 1 else heads * inner[0])
+        _same_device(kc, ks, vc, vs)
+        return _CKVPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *strides, pages,
+                         heads, ps, d, _DT[ks.dtype])
+
+
+def kv_paged_int8(pages: int, heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16,
+                  device="cuda") -> KVPagedInt8:
+    """An empty (zeroed) pool."""
+    shape = (pages, heads, page_size, head_dim)
+    return KVPagedInt8(torch.zeros(shape, dtype=torch.int8, device=device),
+                       torch.zeros(shape[:3], dtype=dtype, device=device),
+                       torch.zeros(shape, dtype=torch.int8, device=device),
+                       torch.zeros(shape[:3], dtype=dtype, device=device))
+
+
+def _dense(shape, strides, want) -> bool:
+    """Strides as wanted, but for dimensions of one element."""
+    return all(n <= 1 or s == w for n, s, w in zip(shape, strides, want))
+
+
+def _same_device(first: torch.Tensor, *rest):
+    if not first.is_cuda:
+        raise ValueError("q4 takes device tensors only")
+    dev = first.device
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors of a call must be on one device")
+
+
+class _Call:
+    """The device and stream of a call whose tensors are on ``device``: the
+    stream given, or that device's current one.  Inside the ``with`` block the
+    device is current, and so is the stream for the allocator, so that what the
+    call allocates belongs to the stream that uses it."""
+
+    def __init__(self, device: torch.device, stream):
+        self.device = device
+        cur = torch.cuda.current_stream(device)
+        self.handle = cur.cuda_stream if stream is None else _stream(stream)
+        self._ctx = None
+        if self.handle != cur.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(self.handle, device=device)
+            self._ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+    def workspace(self, need: int) -> torch.Tensor:
+        """A workspace whose counters are zero.  One buffer per device and
+        stream is kept and grown on demand; a captured graph gets one of its
+        own, so no two graphs and no other stream share it."""
+        if torch.cuda.is_current_stream_capturing():
+            buf = torch.empty(need, dtype=torch.uint8, device=self.device)
+            buf[:_WS_COUNTER_BYTES].zero_()
+            return buf
+        key = (self.device.index, self.handle)
+        buf = _stream_workspaces.get(key)
+        if buf is None or buf.numel() < need:
+            buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            _stream_workspaces[key] = buf
+        return buf
+
+
+_WS_COUNTER_BYTES = 256 * 1024  # the counters at the head of a workspace
+_stream_workspaces: dict = {}
+
+
+def _head_rows(t: torch.Tensor, what: str, heads: int | None, d: int, dtype, tokens: int | None = None):
+    """Checks [tokens, heads, head_dim] with dense heads; returns the row stride."""
+    if t.dim() != 3 or t.dtype != dtype or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
+            or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] in the cache type")
+    n, h, _ = t.shape
+    st = t.stride()
+    if not _dense((h, d), st[1:], (d, 1)):
+        raise ValueError(f"{what}: the heads of a token must be dense")
+    return st[0] if n > 1 else h * d
+
+
+def _int32(t: torch.Tensor | None, what: str, shape):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+
+
+def _kv_batch(block_table, seq_lens, cu_new, tokens: int, max_new: int) -> _CKVBatch:
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs, width]")
+    seqs, width = block_table.shape
+    _int32(block_table, "block_table", (seqs, width))
+    _int32(seq_lens, "seq_lens", (seqs,))
+    _int32(cu_new, "cu_new", (seqs + 1,))
+    return _CKVBatch(block_table.data_ptr(), seq_lens.data_ptr(),
+                     cu_new.data_ptr() if cu_new is not None else None, width, tokens, max_new, seqs)
+
+
+def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                         slots: torch.Tensor, positions: torch.Tensor | None = None,
+                         inv_freq: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+                         k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                         interleaved: bool = False, q_out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor | None:
+    """The new tokens of a layer into its cache: query / key RMS norm (where a
+    weight is given), rotation by position (where inv_freq [rot_dim / 2] is),
+    INT8 quantization of k and v into slots (int64 [tokens], page * page_size +
+    offset, negative: padding).  q [tokens, q_heads, head_dim], k and v
+    [tokens, heads, head_dim]: slices of a fused projection will do.  Returns
+    the queries (q_out, which may be q; None without q)."""
+    lib = load_library()
+    cs = cache.c_struct()
+    dt, d = cache.dtype, cs.head_dim
+    tokens = k.shape[0]
+    ks = _head_rows(k, "k", cs.heads, d, dt)
+    vs = _head_rows(v, "v", cs.heads, d, dt, tokens)
+    qs = _head_rows(q, "q", None, d, dt, tokens) if q is not None else 0
+    if slots.dtype != torch.int64 or tuple(slots.shape) != (tokens,) or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int64 [tokens]")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous fp32 [rot_dim / 2]")
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        rot = 2 * inv_freq.shape[0]
+        _int32(positions, "positions", (tokens,))
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype != dt or tuple(w.shape) != (d,) or not w.is_contiguous()):
+            raise ValueError("norm weights must be [head_dim] in the cache type")
+    _same_device(cache.k_codes, q, k, v, slots, positions, inv_freq, q_norm, k_norm, q_out)
+    with _Call(k.device, stream) as call:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        os_ = _head_rows(q_out, "q_out", q.shape[1], d, dt, tokens) if q is not None else 0
+        st = lib.kv_append_int8_paged(
+            ctypes.byref(cs), q.data_ptr() if q is not None else None, qs,
+            q.shape[1] if q is not None else 0, k.data_ptr(), ks, v.data_ptr(), vs, tokens,
+            slots.data_ptr(), positions.data_ptr() if positions is not None else None,
+            inv_freq.data_ptr() if inv_freq is not None else None, rot, int(interleaved),
+            q_norm.data_ptr() if q_norm is not None else None,
+            k_norm.data_ptr() if k_norm is not None else None, eps,
+            q_out.data_ptr() if q is not None else None, os_, call.handle)
+    _check(st, "kv_append_int8_paged")
+    return q_out
+
+
+def kv_gather_int8_paged(cache: KVPagedInt8, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+                         v_out: torch.Tensor | None = None, stream=None):
+    """(k, v) [tokens, heads, head_dim]: the dequantized rows of slots (rows of
+    negative slots are left as they are)."""
+    lib = load_library()
+    cs = cache.c_struct()
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int64 [tokens]")
+    shape = (slots.shape[0], cs.heads, cs.head_dim)
+    _same_device(cache.k_codes, slots, k_out, v_out)
+    with _Call(slots.device, stream) as call:
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=cache.dtype, device=slots.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=cache.dtype, device=slots.device)
+        for x in (k_out, v_out):
+            if x.dtype != cache.dtype or tuple(x.shape) != shape or not x.is_contiguous():
+                raise ValueError("k_out and v_out must be contiguous [tokens, heads, head_dim] in the cache type")
+        st = lib.kv_gather_int8_paged(ctypes.byref(cs), slots.data_ptr(), shape[0], k_out.data_ptr(),
+                                      v_out.data_ptr(), call.handle)
+    _check(st, "kv_gather_int8_paged")
+    return k_out, v_out
+
+
+def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
+                            max_new: int = 1, scale: float | None = None, window: int = 0,
+                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """(out, lse): causal attention of each sequence's new tokens (rows
+    cu_new[b] .. cu_new[b + 1] - 1 of q; None: row b) over its seq_lens[b]
+    cached tokens, the new ones among them; the last ``window`` of those a token
+    sees, if given.  scale defaults to head_dim ** -0.5.  max_new: the most new
+    tokens of a sequence.  A workspace of your own has its first 256 KiB zero."""
+    lib = load_library()
+    cs = cache.c_struct()
+    d, dt, tokens = cs.head_dim, cache.dtype, q.shape[0]
+    qs = _head_rows(q, "q", None, d, dt)
+    hq = q.shape[1]
+    batch = _kv_batch(block_table, seq_lens, cu_new, tokens, max_new)
+    _same_device(cache.k_codes, q, block_table, seq_lens, cu_new, out, lse, workspace)
+    with _Call(q.device, stream) as call:
+        if out is None:
+            out = torch.empty(q.shape, dtype=dt, device=q.device)
+        if lse is None:
+            lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, hq) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [tokens, q_heads]")
+        os_ = _head_rows(out, "out", hq, d, dt, tokens)
+        if workspace is None:
+            workspace = call.workspace(
+                int(lib.kv_attention_workspace_bytes(d, hq, cs.heads, max(1, min(max_new, tokens)))))
+        st = lib.kv_attention_int8_paged(
+            ctypes.byref(cs), q.data_ptr(), qs, hq, ctypes.byref(batch),
+            d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), call.handle)
+    _check(st, "kv_attention_int8_paged")
+    return out, lse
+
+
+def kv_attention_mass_int8_paged(cache: KVPagedInt8, q: torch.Tensor, lse: torch.Tensor,
+                                 mass: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
+                                 max_new: int = 1, scale: float | None = None, window: int = 0,
+                                 stream=None) -> torch.Tensor:
+    """Adds to mass (fp32 [pages, heads, page_size]) the attention weight that
+    each cached token received from these queries; lse as the attention call
+    with the same arguments returned it.  Returns mass."""
+    lib = load_library()
+    cs = cache.c_struct()
+    tokens, hq = q.shape[0], q.shape[1]
+    qs = _head_rows(q, "q", None, cs.head_dim, cache.dtype)
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, hq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [tokens, q_heads]")
+    ms = _mass_stride(cache, mass)
+    batch = _kv_batch(block_table, seq_lens, cu_new, tokens, max_new)
+    _same_device(cache.k_codes, q, lse, mass, block_table, seq_lens, cu_new)
+    with _Call(q.device, stream) as call:
+        st = lib.kv_attention_mass_int8_paged(
+            ctypes.byref(cs), q.data_ptr(), qs, hq, lse.data_ptr(), ctypes.byref(batch),
+            cs.head_dim ** -0.5 if scale is None else scale, window, mass.data_ptr(), ms, call.handle)
+    _check(st, "kv_attention_mass_int8_paged")
+    return mass
+
+
+def _mass_stride(cache: KVPagedInt8, mass: torch.Tensor) -> int:
+    pages, heads, ps = cache.k_scales.shape
+    if mass.dtype != torch.float32 or tuple(mass.shape) != (pages, heads, ps) \
+            or not _dense((heads, ps), mass.stride()[1:], (ps, 1)):
+        raise ValueError("mass must be fp32 [pages, heads, page_size], a page dense")
+    return mass.stride(0) if pages > 1 else heads * ps
+
+
+def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: torch.Tensor,
+                        seq_lens: torch.Tensor, budget: int, recent: int = 0, sinks: int = 0,
+                        dst_table: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Cuts every sequence to ``budget`` tokens per KV head: the first
+    ``sinks``, the last ``recent`` and the heaviest of the others by mass, moved
+    in order into the pages of dst_table (None: in place).  Returns the new
+    lengths (int32 [seqs])."""
+    lib = load_library()
+    cs = cache.c_struct()
+    ms = _mass_stride(cache, mass)
+    batch = _kv_batch(block_table, seq_lens, None, 0, 1)
+    seqs = batch.seqs
+    if dst_table is not None:
+        if dst_table.dim() != 2:
+            raise ValueError("dst_table must be [seqs, width]")
+        _int32(dst_table, "dst_table", (seqs, dst_table.shape[1]))
+    _int32(new_lens, "new_lens", (seqs,))
+    _same_device(cache.k_codes, mass, block_table, seq_lens, dst_table, new_lens, workspace)
+    with _Call(seq_lens.device, stream) as call:
+        if new_lens is None:
+            new_lens = torch.empty(seqs, dtype=torch.int32, device=seq_lens.device)
+        if workspace is None:
+            need = int(lib.kv_evict_workspace_bytes(seqs, cs.heads, budget))
+            workspace = torch.empty(need, dtype=torch.uint8, device=seq_lens.device)
+        st = lib.kv_evict_int8_paged(
+            ctypes.byref(cs), mass.data_ptr(), ms, ctypes.byref(batch), budget, recent, sinks,
+            dst_table.data_ptr() if dst_table is not None else None,
+            dst_table.shape[1] if dst_table is not None else 0, new_lens.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), call.handle)
+    _check(st, "kv_evict_int8_paged")
+    return new_lens
 
 
 # ------------------------------------------------------ FP4 microscaling

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libq4.so")
-SOURCES = [os.path.join(CSRC, "q4_api.cu")]
+SOURCES = [os.path.join(CSRC, "q4_api.cu"), os.path.join(CSRC, "kv_api.cu")]
 DEPS = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "q4.h")]
 
 
@@ -34,7 +34,7 @@ def flags(verbose_ptxas: bool = False) -> list[str]:
         "-Xcompiler", "-fPIC,-fvisibility=hidden",
         "--expt-relaxed-constexpr",
         "-I", INCLUDE, "-I", CSRC,
-        "-shared", "-cudart", "static",
+        "-cudart", "static",
     ]
     if verbose_ptxas:
         f += ["-Xptxas", "-v"]
@@ -51,15 +51,22 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
-    os.close(fd)
-    cmd = [nvcc_path(), *flags(verbose_ptxas), *SOURCES, "-o", tmp, "-ldl", "-lpthread", "-lrt"]
-    try:
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, LIB)
-    finally:
-        if os.path.exists(tmp):
-            os.remove(tmp)
+    base = [nvcc_path(), *flags(verbose_ptxas)]
+    with tempfile.TemporaryDirectory() as objs:
+        outs = [os.path.join(objs, os.path.basename(src) + ".o") for src in SOURCES]
+        jobs = [subprocess.Popen([*base, "-c", src, "-o", o]) for src, o in zip(SOURCES, outs)]
+        codes = [j.wait() for j in jobs]
+        for src, rc in zip(SOURCES, codes):
+            if rc:
+                raise subprocess.CalledProcessError(rc, f"nvcc -c {src}")
+        fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+        os.close(fd)
+        try:
+            subprocess.run([*base, "-shared", *outs, "-o", tmp, "-ldl", "-lpthread", "-lrt"], check=True)
+            os.replace(tmp, LIB)
+        finally:
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return LIB
 
 

@@ -43,6 +43,7 @@
 #include "q4_device.cuh"
 #include "q4_gemv.cuh"
 #include "q4_gemv_sk.cuh"
+#include "q8_codes.cuh"
 
 namespace q4dev {
 
@@ -63,19 +64,6 @@ __host__ __device__ inline Q8Geom q8_geom(int rt, int stages) {
     g.off_bar = g.stage_bytes * stages;
     g.total = g.off_bar + static_cast<size_t>(2 * kQ8MaxStages) * 8 + 64 + 1024;
     return g;
-}
-
-// Two codes of a word (bytes selected by `sel`: 0x4140 for bytes 0, 1 and
-// 0x4342 for bytes 2, 3) as a pair of exact 16-bit floats.
-template <bool BF16>
-__device__ __forceinline__ uint32_t q8_pair(uint32_t w, uint32_t sel) {
-    if constexpr (BF16) {
-        const uint32_t p = prmt(w, 0x43u, sel);  // 0x43 b' 0x43 b
-        return sub2<true>(p & 0xFF7FFF7Fu, p & 0xFF80FF80u);
-    } else {
-        const uint32_t p = prmt(w, 0x64u, sel) ^ 0x00800080u;
-        return sub2<false>(p, 0x64806480u);
-    }
 }
 
 // Four MMAs of one 16-byte unit per row: wa, wb the units of rows R0 and

@@ -18,37 +18,11 @@
 
 #include "q4_device.cuh"
 #include "q4_quant.cuh"
+#include "q8_codes.cuh"
 
 namespace q4dev {
 
 // ---------------------------------------------------------- INT8 weights
-
-// INT8 code of one value, clamp(rne(fl(v / s)), qmin, 127), through t = v * r
-// (r = 1/s correctly rounded, from quot_recip): |t - fl(v/s)| <= |t| (3u + u^2)
-// (u = 2^-24), below 3.2e-5 while |t| < 178, and t - rint(t) is exact; so when
-// |t - rint(t)| < 0.5 - 3.2e-5 both round to the same integer, and from
-// |t| >= 178 on both clamp alike.  Otherwise (near a tie, or a NaN) the exact
-// quotient is rounded as the definition states (NaN -> qmin).
-__device__ __forceinline__ int int8_code(float v, float s, float r, int qmin) {
-    const float t = __fmul_rn(v, r);
-    const int q = __float2int_rn(t);
-    if (fabsf(__fsub_rn(t, __int2float_rn(q))) < 0.4999679f) return min(max(q, qmin), 127);
-    float u = rintf(__fdiv_rn(v, s));
-    u = fminf(fmaxf(u, static_cast<float>(qmin)), 127.f);
-    return static_cast<int>(u);
-}
-
-// Eight codes as two little-endian words (element 0 in byte 0).
-__device__ __forceinline__ uint2 pack8_bytes(const int (&q)[8]) {
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __byte_perm(q[4 * h], q[4 * h + 1], 0x0040);
-        const uint32_t hi = __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040);
-        w[h] = __byte_perm(lo, hi, 0x5410);
-    }
-    return make_uint2(w[0], w[1]);
-}
 
 // One CTA per row (grid-stride over rows): the row's amax by a block
 // reduction, then the codes; the second read of the row comes from L2.
@@ -133,26 +107,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------- INT8 KV cache
-
-template <bool BF16>
-__device__ __forceinline__ uint16_t cache_bits(float v) {
-    if constexpr (BF16) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        return *reinterpret_cast<const uint16_t*>(&h);
-    } else {
-        const __half h = __float2half_rn(v);
-        return *reinterpret_cast<const uint16_t*>(&h);
-    }
-}
-template <bool BF16>
-__device__ __forceinline__ float cache_value(uint16_t b) {
-    if constexpr (BF16) {
-        return __uint_as_float(static_cast<uint32_t>(b) << 16);
-    } else {
-        return __half2float(__ushort_as_half(b));
-    }
-}
-
 
 // A team of TS lanes (a power of two dividing 32) per row of d values; a lane
 // holds the 8-value vectors sub and sub + TS of the row (d <= 16 * TS).  The
