@@ -14,6 +14,7 @@
 #include "q4_host.cuh"
 #include "kv_paged.cuh"
 #include "kv_attention.cuh"
+#include "kv_attention_tc.cuh"
 #include "kv_mass.cuh"
 #include "kv_evict.cuh"
 
@@ -99,8 +100,14 @@ int team_size(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
 // ------------------------------------------------------------- attention
 
+// Which kernel: the tensor-core one from more than kTcMinRows rows of a
+// sequence and KV head on (head_dim up to 128), the other for decode steps.
+constexpr int64_t kTcMinRows = 16;
+
 struct AttnPlan {
-    int nr;               // blocks of 8 rows of a unit
+    bool tc;
+    int nr;               // the other kernel's blocks of 8 rows of a unit
+    int rows;             // rows of a unit
     int64_t ctas;         // at most so many
     size_t slot, bytes;   // floats of a partial slot; workspace bytes
 };
@@ -108,9 +115,11 @@ struct AttnPlan {
 AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
     AttnPlan p{};
     const int dp = padded_dim(d);
+    p.tc = dp <= 128 && max_new * group > kTcMinRows;
     p.nr = max_new * group <= 8 ? 1 : 2;
-    p.ctas = static_cast<int64_t>(dp * p.nr > 128 ? 1 : 2) * sms;
-    p.slot = static_cast<size_t>(8 * p.nr) * (dp + 2);
+    p.rows = p.tc ? kTcaRows : 8 * p.nr;
+    p.ctas = static_cast<int64_t>(p.tc || dp * p.nr > 128 ? 1 : 2) * sms;
+    p.slot = static_cast<size_t>(p.rows) * (dp + 2);
     p.bytes = kWsCounterBytes + 2 * static_cast<size_t>(p.ctas) * p.slot * 4;
     return p;
 }
@@ -124,9 +133,20 @@ q4_status run_attention(const KvAttn& a, int64_t grid, cudaStream_t st) {
                      st, a);
 }
 
+template <bool BF16, int DP>
+q4_status run_attention_tc(const KvAttn& a, int64_t grid, cudaStream_t st) {
+    constexpr size_t smem = TcaGeom<DP>::total;
+    auto kernel = kv_attention_tc_kernel<BF16, DP>;
+    if (!set_kernel_attrs(kernel, static_cast<int>(smem), false)) return Q4_ERR_CUDA;
+    return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kTcaThreads), smem, 1, true, st, a);
+}
+
 template <bool BF16>
-q4_status dispatch_attention(const KvAttn& a, int nr, int64_t grid, cudaStream_t st) {
-    switch (padded_dim(a.pool.d)) {
+q4_status dispatch_attention(const KvAttn& a, const AttnPlan& p, int64_t grid, cudaStream_t st) {
+    const int dp = padded_dim(a.pool.d), nr = p.nr;
+    if (p.tc)
+        return dp == 64 ? run_attention_tc<BF16, 64>(a, grid, st) : run_attention_tc<BF16, 128>(a, grid, st);
+    switch (dp) {
         case 64: return nr == 1 ? run_attention<BF16, 64, 1>(a, grid, st)
                                 : run_attention<BF16, 64, 2>(a, grid, st);
         case 128: return nr == 1 ? run_attention<BF16, 128, 1>(a, grid, st)
@@ -294,7 +314,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     KvAttn a{};
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
-    a.geom = {8 * p.nr, kKvTile, group, cache->heads,
+    a.geom = {p.rows, kKvTile, group, cache->heads,
               static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2))};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
@@ -310,12 +330,12 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     if (!a.status) return Q4_ERR_CUDA;
     // no more CTAs than there can be tiles
     const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
-    const int64_t row_tiles = batch->seqs + batch->tokens * group / (8 * p.nr);
+    const int64_t row_tiles = batch->seqs + batch->tokens * group / p.rows;
     int64_t grid = p.ctas;
     if (row_tiles * cache->heads < grid) grid = std::min(grid, row_tiles * cache->heads * tiles);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return cache->dtype == Q4_BF16 ? dispatch_attention<true>(a, p.nr, grid, st)
-                                   : dispatch_attention<false>(a, p.nr, grid, st);
+    return cache->dtype == Q4_BF16 ? dispatch_attention<true>(a, p, grid, st)
+                                   : dispatch_attention<false>(a, p, grid, st);
 }
 
 q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q, int64_t q_stride,
