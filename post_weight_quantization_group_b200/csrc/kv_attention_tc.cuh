@@ -13,9 +13,11 @@
 //   warps 0-3 / 4-7   softmax of half A / B
 //   warps 8-11        conversion: codes from the pages (16-byte loads, a tile
 //                     ahead in registers) to 16-bit floats in shared memory,
-//                     K in the cache type, V in fp16; the tile's scales; the
-//                     unit's Q
+//                     K in the cache type, V in fp16; the unit's Q
 //   warp 12           tcgen05.mma issue
+//   warp 13           walks the CTA's work and leaves for the others, ahead of
+//                     them, its segments (TcaSeg) and the tiles' row addresses
+//                     (block table) and scales
 //
 // K [token, d] is a K-major operand of S and V [token, d] an N-major operand
 // of P V: the same storage, [d / 64] blocks of 128-byte rows, one per token,
@@ -33,16 +35,67 @@ constexpr int kTcaThreads = 512;
 constexpr int kTcaRows = 256;
 constexpr int kTcaKT = 128;  // tokens of a tile
 
+constexpr int kTcaRowSlots = 3;  // tiles of row addresses
+constexpr int kTcaScSlots = 4;   // tiles of scales
+constexpr int kTcaSegSlots = 4;  // segments
+
+// Consecutive tiles of one unit, the work of a CTA one after another; tiles =
+// 0 ends the list.
+struct TcaSeg {
+    int64_t first;             // the sequence's first row of q
+    int past;                  // cached tokens before its new ones
+    int rows, row0, h;         // rows of the sequence and head, the unit's first, the head
+    int tile0, tiles;
+    int first_cta, last_cta;   // the CTAs that share the unit
+    int whole;                 // it is all this CTA's
+    int slot, first_slot;      // partial slot (0 or 1) of this CTA and of first_cta
+    int pad[3];
+};
+static_assert(sizeof(TcaSeg) == 64, "segment ring");
+
 template <int DP>
 struct TcaGeom {
     static constexpr uint32_t tile = DP * 256;  // bytes of 128 rows of DP 16-bit elements
     static constexpr uint32_t off_q = 0;        // two halves
     static constexpr uint32_t off_k = 2 * tile; // two stages
     static constexpr uint32_t off_v = 4 * tile;
-    static constexpr uint32_t off_sc = 6 * tile;                 // two slots of sk, lg, inv
-    static constexpr uint32_t off_bar = off_sc + 2 * 3 * 128 * 4;
-    static constexpr uint32_t total = off_bar + 256 + 1024;
+    static constexpr uint32_t off_sc = 6 * tile;                          // sk, lg, inv [128]
+    static constexpr uint32_t off_row = off_sc + kTcaScSlots * 3 * 128 * 4;  // K, V offsets [128]
+    static constexpr uint32_t off_bar = off_row + kTcaRowSlots * 2 * 128 * 8;
+    static constexpr uint32_t off_seg = off_bar + 512;
+    static constexpr uint32_t total = off_seg + kTcaSegSlots * 64 + 1024;
 };
+
+// Packed fp32 pairs: one instruction for both.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float f_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// An fp32 pair from shared memory.
+__device__ __forceinline__ uint64_t lds_f2(uint32_t addr) {
+    uint64_t v;
+    asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(addr));
+    return v;
+}
 
 // Sixteen codes of token `row`, unit `u` of its DP / 16, as 16-bit floats into
 // a tile.  The second half of a 128-element row stores its chunks in the other
@@ -90,18 +143,25 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::off_bar);
-    uint64_t* k_full = bars;        // [2] conversion -> MMA, softmax (scales)
+    uint64_t* k_full = bars;        // [2] conversion -> MMA
     uint64_t* k_empty = bars + 2;   // [2] S of both halves done
     uint64_t* v_full = bars + 4;    // [2]
     uint64_t* v_empty = bars + 6;   // [2] P V of both halves done
-    uint64_t* sc_free = bars + 8;   // [2] softmax has read the slot's scales
-    uint64_t* s_full = bars + 10;   // [half]
-    uint64_t* p_ready = bars + 12;  // [half]
-    uint64_t* pv_done = bars + 14;  // [half]
-    uint64_t* q_full = bars + 16;
-    uint64_t* q_free = bars + 17;
-    uint64_t* drain = bars + 18;
-    uint32_t* tbase_s = reinterpret_cast<uint32_t*>(bars + 19);
+    uint64_t* s_full = bars + 8;    // [half]
+    uint64_t* p_ready = bars + 10;  // [half]
+    uint64_t* pv_done = bars + 12;  // [half]
+    uint64_t* q_full = bars + 14;
+    uint64_t* q_free = bars + 15;
+    uint64_t* drain = bars + 16;
+    uint64_t* sc_full = bars + 17;             // [kTcaScSlots]
+    uint64_t* sc_free = sc_full + kTcaScSlots;
+    uint64_t* row_full = sc_free + kTcaScSlots;  // [kTcaRowSlots]
+    uint64_t* row_free = row_full + kTcaRowSlots;
+    uint64_t* seg_full = row_free + kTcaRowSlots;  // [kTcaSegSlots]
+    uint64_t* seg_free = seg_full + kTcaSegSlots;
+    uint64_t* join = seg_free + kTcaSegSlots;  // [2] the halves' parts are stored; the count is known
+    uint32_t* tbase_s = reinterpret_cast<uint32_t*>(join + 2);
+    TcaSeg* segs = reinterpret_cast<TcaSeg*>(smem + G::off_seg);
     __shared__ KvLocateShared s_loc;
     __shared__ unsigned s_last;
 
@@ -112,11 +172,24 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 4);
             mbar_init(&v_empty[i], 1);
-            mbar_init(&sc_free[i], 8);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
             mbar_init(&pv_done[i], 1);
         }
+        for (int i = 0; i < kTcaScSlots; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_free[i], 8);
+        }
+        for (int i = 0; i < kTcaRowSlots; ++i) {
+            mbar_init(&row_full[i], 1);
+            mbar_init(&row_free[i], 4);
+        }
+        for (int i = 0; i < kTcaSegSlots; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_free[i], 13);  // 8 softmax and 4 conversion warps, the MMA thread
+        }
+        mbar_init(&join[0], 8);
+        mbar_init(&join[1], 1);
         mbar_init(q_full, 4);
         mbar_init(q_free, 1);
         mbar_init(drain, 1);
@@ -136,426 +209,586 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                            &end, &w);
     const int group = a.geom.group, window = a.geom.window;
 
-    // Every role walks the same segments: (unit, tiles) of this CTA's range.
-    struct Segment {
-        KvSeq seq;
-        int tile0, tiles, rows, row0;
-        int64_t unit_beg, unit_end;
-        bool both;  // half B has rows
-    };
-    auto segment = [&](int64_t it, const KvPlace& p, const KvSeq& s) {
-        Segment g;
-        int lo;
-        const int n = kv_tiles(a.geom, s, p.rt, &lo);
-        g.seq = s;
-        g.tile0 = lo + p.tile;
-        g.unit_beg = it - p.tile;
-        g.unit_end = g.unit_beg + n;
-        g.tiles = static_cast<int>(min(g.unit_end, end) - it);
-        g.rows = s.n * group;
-        g.row0 = p.rt * kTcaRows;
-        g.both = g.rows - g.row0 > 128;
-        return g;
-    };
-
-    if (beg < end) {
-        KvSeq seq = kv_seq(a.batch, w.b, a.status);
-        if (warp < 8) {
-            // ------------------------------------------------------ softmax
-            regs_inc<184>();
-            const int half = warp >> 2;
-            const uint32_t tl = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-            const uint32_t ts = tl + half * 128, to = tl + kColO + half * DP;
-            const int r = half * 128 + (warp & 3) * 32 + lane;  // row of the unit
-            int c = 0;        // tiles so far: the K stage and scale slot
-            uint32_t n = 0;   // tiles of this half so far
-            bool ok = true;
-            for (int64_t it = beg; it < end;) {  // a failed wait still goes through the barriers
-                const Segment g = segment(it, w, seq);
-                const bool active = half == 0 || g.both;
-                const bool live = g.row0 + r < g.rows;
-                const bool warp_live = g.row0 + r - lane < g.rows;
-                const int past = g.seq.len - g.seq.n;
-                const int at = live ? past + (g.row0 + r) / group : -1;
-                const int at_min = past + (g.row0 + half * 128) / group;
-                const int at_max = past + (min(g.row0 + half * 128 + 128, g.rows) - 1) / group;
-                float m = kKvNone, l = 0.f;
-                for (int i = 0; i < g.tiles && ok; ++i, ++c) {
-                    const int slot = c & 1;
-                    if (active) ok = warp_wait(&s_full[half], n, a.status);
-                    if (ok) ok = warp_wait(&k_full[slot], c >> 1, a.status);
-                    if (!ok) break;
-                    if (!active || !warp_live) {
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&sc_free[slot]);
-                            if (active) mbar_arrive(&p_ready[half]);
-                        }
-                        if (active) ++n;
-                        continue;
-                    }
-                    tc_fence_after();
-                    const float* sc = reinterpret_cast<const float*>(smem + G::off_sc) + slot * 384;
-                    float x[128];
+    if (warp < 8) {
+        // ------------------------------------------------------ softmax
+        regs_inc<152>();
+        const int half = warp >> 2;
+        const uint32_t tl = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t ts = tl + half * 128, to = tl + kColO + half * DP;
+        const int r = half * 128 + (warp & 3) * 32 + lane;  // row of the unit
+        int c = 0;        // tiles so far: the scale slot
+        uint32_t n = 0;   // tiles of this half so far
+        bool ok = true;
+        uint32_t parts = 0;  // shared units so far
+        // the value of row `lane` of the warp, from the quad that holds it as its k-th
+        auto by_lane = [&](const float (&v)[4]) {
+            const int src = (lane & 7) * 4;
+            float y = __shfl_sync(0xFFFFFFFFu, v[0], src);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tmem_ld32(ts + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * q]));
-                    tmem_wait_ld();
-                    const int j0 = (g.tile0 + i) * kTcaKT;
-                    float mx = kKvNone;
+            for (int k = 1; k < 4; ++k) {
+                const float z = __shfl_sync(0xFFFFFFFFu, v[k], src);
+                if ((lane >> 3) == k) y = z;
+            }
+            return y;
+        };
+        // no warp waits without a limit: one that gave up leaves the others to theirs
+        for (int sg = 0;; ++sg) {
+            if (!warp_wait(&seg_full[sg % kTcaSegSlots], sg / kTcaSegSlots, a.status)) break;
+            const volatile TcaSeg& g = segs[sg % kTcaSegSlots];
+            const int tiles = g.tiles, tile0 = g.tile0;
+            if (tiles == 0) break;
+            const bool active = half == 0 || g.rows - g.row0 > 128;
+            const bool warp_live = g.row0 + r - lane < g.rows;
+            // last visible token of this thread's rows 8 k + lane / 4
+            int at[4];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        const float4 sk = *reinterpret_cast<const float4*>(sc + 4 * q);
-                        const float4 lg = *reinterpret_cast<const float4*>(sc + 128 + 4 * q);
-                        x[4 * q] = fmaf(x[4 * q], sk.x, lg.x);
-                        x[4 * q + 1] = fmaf(x[4 * q + 1], sk.y, lg.y);
-                        x[4 * q + 2] = fmaf(x[4 * q + 2], sk.z, lg.z);
-                        x[4 * q + 3] = fmaf(x[4 * q + 3], sk.w, lg.w);
-                    }
-                    // every row of the half sees the whole tile, or masks
-                    if (!(j0 + kTcaKT - 1 <= at_min && (!window || j0 > at_max - window))) {
-                        const int hi = at - j0;                       // columns <= hi
-                        const int lo = window ? at - window - j0 : -1;  // and > lo
-#pragma unroll
-                        for (int q = 0; q < 128; ++q)
-                            if (q > hi || q <= lo) x[q] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 128; ++q) mx = fmaxf(mx, x[q]);
-                    if (__any_sync(0xFFFFFFFFu, mx > m + kKvLazy)) {
-                        const float mn = fmaxf(m, mx), f = kv_exp2(m - mn);
-                        m = mn;
-                        l *= f;
-                        if (i > 0) {
-                            ok = warp_wait(&pv_done[half], n - 1, a.status);
-                            tc_fence_after();
-#pragma unroll
-                            for (int q = 0; q < DP / 16; ++q) {
-                                uint32_t o[16];
-                                tmem_ld16(to + 16 * q, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st8(to + 16 * q, *reinterpret_cast<uint32_t(*)[8]>(&o[0]));
-                                tmem_st8(to + 16 * q + 8, *reinterpret_cast<uint32_t(*)[8]>(&o[8]));
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int y = 64 * q + 4 * e;
-                            const float4 inv = *reinterpret_cast<const float4*>(sc + 256 + y);
-                            const float p0 = kv_exp2(x[y] - m), p1 = kv_exp2(x[y + 1] - m);
-                            const float p2 = kv_exp2(x[y + 2] - m), p3 = kv_exp2(x[y + 3] - m);
-                            l = fmaf(p0, inv.x, l);
-                            l = fmaf(p1, inv.y, l);
-                            l = fmaf(p2, inv.z, l);
-                            l = fmaf(p3, inv.w, l);
-                            p[2 * e] = kv_pack_f16(p0, p1);
-                            p[2 * e + 1] = kv_pack_f16(p2, p3);
-                        }
-                        tmem_st32(ts + 32 * q, p);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
+            for (int k = 0; k < 4; ++k) {
+                const int rr = g.row0 + r - lane + 8 * k + (lane >> 2);
+                at[k] = rr < g.rows ? g.past + rr / group : -1;
+            }
+            // a tile at j0 is open to every row of the half if j0 <= open_hi, > open_lo
+            const int open_hi = g.past + (g.row0 + half * 128) / group - (kTcaKT - 1);
+            const int open_lo =
+                window ? g.past + (min(g.row0 + half * 128 + 128, g.rows) - 1) / group - window : -1;
+            float m[4] = {kKvNone, kKvNone, kKvNone, kKvNone};
+            uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+            for (int i = 0; i < tiles && ok; ++i, ++c) {
+                const int slot = c % kTcaScSlots;
+                if (active) ok = warp_wait(&s_full[half], n, a.status);
+                if (ok) ok = warp_wait(&sc_full[slot], c / kTcaScSlots, a.status);
+                if (!ok) break;
+                if (!active || !warp_live) {
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&p_ready[half]);
                         mbar_arrive(&sc_free[slot]);
+                        if (active) mbar_arrive(&p_ready[half]);
                     }
-                    ++n;
+                    if (active) ++n;
+                    continue;
                 }
-                // ------------------------------------- end of the segment
-                const bool whole = it == g.unit_beg && it + g.tiles == g.unit_end;
-                const int row = g.row0 + r, tok = row / group;
-                const int head = w.h * group + row - tok * group;
-                uint16_t* out = a.out + (g.seq.first + tok) * a.out_stride + static_cast<int64_t>(head) * a.pool.d;
-                auto store_lse = [&](float mm, float ll) {
-                    if (a.lse)
-                        a.lse[(g.seq.first + tok) * a.q_heads + head] =
-                            ll == 0.f ? -INFINITY : 0.69314718f * (mm + __log2f(ll));
+                tc_fence_after();
+                const uint32_t sc = sbase + G::off_sc + slot * 1536u + (lane & 3) * 8u;
+                const int j0 = (tile0 + i) * kTcaKT;
+                const bool open = j0 <= open_hi && j0 > open_lo;
+                // S of columns 32 q .. 32 q + 31: the warp's lanes 0-15, then 16-31
+                auto read_s = [&](int q, uint32_t (&v)[32]) {
+                    tmem_ld_frag32(ts + 32 * q, v);
+                    tmem_ld_frag32(ts + 32 * q + (16u << 16), v + 16);
                 };
-                // eight elements of the row from column e0 on
-                auto store8 = [&](int e0, float ll, const float (&v)[8]) {
-                    const float inv = ll > 0.f ? __fdiv_rn(1.f, ll) : ll == 0.f ? 0.f : ll;
-                    float y[8];
+                // x = S sk + lg, masked: x[8 e + 2 y + z] of row 8 (2 e + z) + lane / 4 and the
+                // columns 32 q + 8 y + 2 (lane % 4), + 1
+                auto scores = [&](int q, const uint32_t (&v)[32], uint64_t (&x)[16]) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = v[e] * inv;
-                    if (e0 < a.pool.d) *reinterpret_cast<uint4*>(out + e0) = pack8<BF16>(y);
-                };
-                const int64_t first_cta = whole ? 0 : kv_owner(g.unit_beg, T, P);
-                const int64_t last_cta = whole ? 0 : kv_owner(g.unit_end - 1, T, P);
-                if (ok && active && warp_live) {
-                    ok = warp_wait(&pv_done[half], n - 1, a.status);
-                    tc_fence_after();
-                    // a slot: m [256], l [256], O [DP][256] (a column of rows together)
-                    float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (it == beg ? 0 : 1)) * SLOT;
-                    if (whole) {
-                        if (live) store_lse(m, l);
-                    } else {
-                        __stcg(part + r, m);
-                        __stcg(part + kTcaRows + r, l);
-                    }
+                    for (int y = 0; y < 4; ++y) {
+                        const uint64_t sk = lds_f2(sc + 128 * q + 32 * y);
+                        const uint64_t lg = lds_f2(sc + 512 + 128 * q + 32 * y);
 #pragma unroll
-                    for (int q = 0; q < DP / 16; ++q) {
-                        uint32_t o[16];
-                        tmem_ld16(to + 16 * q, o);
-                        tmem_wait_ld();
-                        if (whole) {
-                            if (live) {
-                                store8(16 * q, l, *reinterpret_cast<float(*)[8]>(&o[0]));
-                                store8(16 * q + 8, l, *reinterpret_cast<float(*)[8]>(&o[8]));
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t* w2 = v + 16 * e + 4 * y + 2 * z;
+                                x[8 * e + 2 * y + z] = f2_fma(
+                                    f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])), sk, lg);
                             }
-                        } else {
+                    }
+                    if (!open) {
+                        const int c0 = j0 + 32 * q + 2 * (lane & 3);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                __stcg(part + 2 * kTcaRows + (16 * q + e) * kTcaRows + r, __uint_as_float(o[e]));
+                        for (int e = 0; e < 16; ++e) {
+                            const int col = c0 + 8 * ((e >> 1) & 3), top = at[2 * (e >> 3) + (e & 1)];
+                            float u, t;
+                            f2_unpack(x[e], u, t);
+                            if (col > top || (window && col <= top - window)) u = -INFINITY;
+                            if (col + 1 > top || (window && col + 1 <= top - window)) t = -INFINITY;
+                            x[e] = f2_pack(u, t);
                         }
                     }
-                    tc_fence_before();
+                };
+                uint32_t sv[2][32];
+                float mx[4] = {kKvNone, kKvNone, kKvNone, kKvNone};
+                // two passes over S (maxima, then weights), each chunk read one ahead: the
+                // whole row in registers would spill, and there is next to no L1 to spill to
+                read_s(0, sv[0]);
+#pragma unroll 1
+                for (int q2 = 0; q2 < 4; q2 += 2) {
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        const int q = q2 + h2;
+                        tmem_wait_ld();
+                        read_s((q + 1) & 3, sv[h2 ^ 1]);  // after the last: chunk 0 for the second pass
+                        uint64_t x[16];
+                        scores(q, sv[h2], x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float u, t;
+                            f2_unpack(x[e], u, t);
+                            float& mr = mx[2 * (e >> 3) + (e & 1)];
+                            mr = f_max3(mr, u, t);
+                        }
+                    }
                 }
-                if (!whole) {
-                    named_bar_sync(1, 256);
-                    if (tid == 0) {
+                bool grow = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) grow |= mx[k] > m[k] + kKvLazy;
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    float f[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
+                        const float mn = fmaxf(m[k], mx[k]);
+                        f[k] = kv_exp2(m[k] - mn);
+                        m[k] = mn;
+                        l2[k] = f2_fma(l2[k], f2_pack(f[k], f[k]), 0ull);
+                    }
+                    if (i > 0) {
+                        const float fr = by_lane(f);
+                        ok = warp_wait(&pv_done[half], n - 1, a.status);
+                        tc_fence_after();
+                        tmem_wait_ld();
+#pragma unroll 1
+                        for (int q = 0; q < DP / 8; ++q) {
+                            uint32_t o[8];
+                            tmem_ld8(to + 8 * q, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+                            tmem_st8(to + 8 * q, o);
+                        }
+                    }
+                }
+                // p' of 32 columns go over the S columns 16 q .. 16 q + 15, which have been read
+#pragma unroll 1
+                for (int q2 = 0; q2 < 4; q2 += 2) {
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        const int q = q2 + h2;
+                        tmem_wait_ld();
+                        if (q < 3) read_s(q + 1, sv[h2 ^ 1]);
+                        uint64_t x[16];
+                        scores(q, sv[h2], x);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint64_t inv = lds_f2(sc + 1024 + 128 * q + 32 * y);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    const int k = 2 * e + z;
+                                    float u, t;
+                                    f2_unpack(f2_add(x[8 * e + 2 * y + z], f2_pack(-m[k], -m[k])), u, t);
+                                    u = kv_exp2(u);
+                                    t = kv_exp2(t);
+                                    l2[k] = f2_fma(f2_pack(u, t), inv, l2[k]);
+                                    p[8 * e + 2 * y + z] = kv_pack_f16(u, t);
+                                }
+                        }
+                        tmem_st_frag16(ts + 16 * q, p);
+                        tmem_st_frag16(ts + 16 * q + (16u << 16), p + 8);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&p_ready[half]);
+                    mbar_arrive(&sc_free[slot]);
+                }
+                ++n;
+            }
+            float ms = 0.f, l = 0.f;  // this lane's row's
+            {
+                float ls[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float u, t;
+                    f2_unpack(l2[k], u, t);
+                    ls[k] = u + t;
+                    ls[k] += __shfl_xor_sync(0xFFFFFFFFu, ls[k], 1);
+                    ls[k] += __shfl_xor_sync(0xFFFFFFFFu, ls[k], 2);
+                }
+                l = by_lane(ls);
+                ms = by_lane(m);
+            }
+            // ------------------------------------- end of the segment
+            const bool whole = g.whole != 0;
+            const int row = g.row0 + r, tok = row / group;
+            const bool live = row < g.rows;
+            const int head = g.h * group + row - tok * group;
+            const int64_t qrow = g.first + tok;
+            uint16_t* out = a.out + qrow * a.out_stride + static_cast<int64_t>(head) * a.pool.d;
+            auto store_lse = [&](float mm, float ll) {
+                if (a.lse)
+                    a.lse[qrow * a.q_heads + head] =
+                        ll == 0.f ? -INFINITY : 0.69314718f * (mm + __log2f(ll));
+            };
+            auto inverse = [](float ll) { return ll > 0.f ? __fdiv_rn(1.f, ll) : ll == 0.f ? 0.f : ll; };
+            // eight elements of the row from column e0 on
+            auto store8 = [&](int e0, float inv, const float (&v)[8]) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = v[e] * inv;
+                if (e0 < a.pool.d) *reinterpret_cast<uint4*>(out + e0) = pack8<BF16>(y);
+            };
+            const int first_cta = g.first_cta, last_cta = g.last_cta;
+            if (ok && active && warp_live) {
+                ok = warp_wait(&pv_done[half], n - 1, a.status);
+                tc_fence_after();
+                // a slot: m [256], l [256], O [DP][256] (a column of rows together)
+                float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + g.slot) * SLOT;
+                if (whole) {
+                    if (live) store_lse(ms, l);
+                } else {
+                    __stcg(part + r, ms);
+                    __stcg(part + kTcaRows + r, l);
+                }
+                const float inv = inverse(l);
+#pragma unroll 1
+                for (int q = 0; q < DP / 16; ++q) {
+                    uint32_t o[16];
+                    tmem_ld16(to + 16 * q, o);
+                    tmem_wait_ld();
+                    if (whole) {
+                        if (live) {
+                            store8(16 * q, inv, *reinterpret_cast<float(*)[8]>(&o[0]));
+                            store8(16 * q + 8, inv, *reinterpret_cast<float(*)[8]>(&o[8]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            __stcg(part + 2 * kTcaRows + (16 * q + e) * kTcaRows + r, __uint_as_float(o[e]));
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!whole) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&join[0]);
+                if (warp == 0) {
+                    ok = warp_wait(&join[0], parts, a.status) && ok;
+                    if (lane == 0) {
                         const unsigned prev = kv_arrive(a.count + first_cta);
                         s_last = prev == static_cast<unsigned>(last_cta - first_cta);
                         if (s_last) a.count[first_cta] = 0u;  // zero again for the next call
-                    }
-                    named_bar_sync(1, 256);
-                    if (ok && s_last && active && live) {
-                        __threadfence();
-                        auto slot_of = [&](int64_t p) -> const float* {
-                            return a.part + (2 * p + (T * p / P >= g.unit_beg ? 0 : 1)) * SLOT;
-                        };
-                        float mm = kKvNone;
-                        for (int64_t p = first_cta; p <= last_cta; ++p) mm = fmaxf(mm, __ldcg(slot_of(p) + r));
-                        float ll = 0.f;
-                        for (int64_t p = first_cta; p <= last_cta; ++p) {
-                            const float* s = slot_of(p);
-                            ll = fmaf(__ldcg(s + kTcaRows + r), kv_exp2(__ldcg(s + r) - mm), ll);
-                        }
-                        store_lse(mm, ll);
-                        for (int e0 = 0; e0 < DP; e0 += 8) {
-                            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                            for (int64_t p = first_cta; p <= last_cta; ++p) {
-                                const float* s = slot_of(p);
-                                const float f = kv_exp2(__ldcg(s + r) - mm);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    v[e] = fmaf(f, __ldcg(s + 2 * kTcaRows + (e0 + e) * kTcaRows + r), v[e]);
-                            }
-                            store8(e0, ll, v);
-                        }
+                        mbar_arrive(&join[1]);
                     }
                 }
-                it += g.tiles;
-                if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
-            }
-        } else if (warp < 12) {
-            // --------------------------------------------------- conversion
-            regs_dec<104>();
-            constexpr int UPR = DP / 16;           // 16-code units of a row
-            constexpr int NI = 128 * UPR / 128;    // units of a thread
-            constexpr int RSTEP = 128 / UPR;       // rows between them
-            const KvPool& pc = a.pool;
-            const int ct = tid - 256, u = ct % UPR, rb = ct / UPR;
-            const bool unit_on = u * 16 < pc.d;
-            const int shift = (pc.ps & (pc.ps - 1)) == 0 ? 31 - __clz(pc.ps) : -1;
-            auto entry_of = [&](int j, int* off) {  // table entry and place in the page of token j
-                const int e = shift >= 0 ? j >> shift : j / pc.ps;
-                *off = j - e * pc.ps;
-                return e;
-            };
-            bool ok = true;
-            int c = 0, segs = 0;
-            for (int64_t it = beg; it < end && ok; ++segs) {
-                const Segment g = segment(it, w, seq);
-                uint4 kr[NI], vr[NI];
-                int32_t ent[NI], ent_sc = 0;
-                uint16_t ks = 0, vs = 0;
-                auto entries = [&](int j0) {
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int j = j0 + rb + i * RSTEP;
-                        int off;
-                        ent[i] = j < g.seq.len ? kv_entry(a.batch, w.b, entry_of(j, &off)) : 0;
+                ok = warp_wait(&join[1], parts, a.status) && ok;
+                ++parts;
+                if (ok && s_last && active && live) {
+                    __threadfence();
+                    // only the first of the unit's CTAs can have begun before it
+                    const int first_slot = g.first_slot;
+                    auto slot_of = [&](int p) -> const float* {
+                        return a.part + (2 * static_cast<int64_t>(p) + (p == first_cta ? first_slot : 0)) * SLOT;
+                    };
+                    float mm = kKvNone;
+                    for (int p = first_cta; p <= last_cta; ++p) mm = fmaxf(mm, __ldcg(slot_of(p) + r));
+                    float ll = 0.f;
+                    for (int p = first_cta; p <= last_cta; ++p) {
+                        const float* s = slot_of(p);
+                        ll = fmaf(__ldcg(s + kTcaRows + r), kv_exp2(__ldcg(s + r) - mm), ll);
                     }
-                    int off;
-                    const int j = j0 + ct;
-                    ent_sc = j < g.seq.len ? kv_entry(a.batch, w.b, entry_of(j, &off)) : 0;
-                };
-                auto load = [&](uint4 (&x)[NI], const int8_t* base, int64_t stride, int j0) {
+                    store_lse(mm, ll);
+                    const float inv = inverse(ll);
+                    for (int e0 = 0; e0 < DP; e0 += 8) {
+                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        for (int p = first_cta; p <= last_cta; ++p) {
+                            const float* s = slot_of(p);
+                            const float f = kv_exp2(__ldcg(s + r) - mm);
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int j = j0 + rb + i * RSTEP;
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (j < g.seq.len && unit_on) {
-                            int off;
-                            entry_of(j, &off);
-                            const int64_t page = kv_page(pc, ent[i], a.status);
-                            x[i] = __ldg(reinterpret_cast<const uint4*>(
-                                base + page * stride + kv_row(pc, w.h, off) * pc.d + u * 16));
+                            for (int e = 0; e < 8; ++e)
+                                v[e] = fmaf(f, __ldcg(s + 2 * kTcaRows + (e0 + e) * kTcaRows + r), v[e]);
                         }
+                        store8(e0, inv, v);
                     }
-                };
-                auto load_scales = [&](int j0) {
-                    const int j = j0 + ct;
-                    ks = vs = 0;
-                    if (j < g.seq.len) {
-                        int off;
-                        entry_of(j, &off);
-                        const int64_t page = kv_page(pc, ent_sc, a.status), row = kv_row(pc, w.h, off);
-                        ks = __ldg(pc.ks + page * pc.ks_page + row);
-                        vs = __ldg(pc.vs + page * pc.vs_page + row);
-                    }
-                };
-                int j0 = g.tile0 * kTcaKT;
-                entries(j0);
-                load(kr, pc.kc, pc.kc_page, j0);
-                load_scales(j0);
-                load(vr, pc.vc, pc.vc_page, j0);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_free[sg % kTcaSegSlots]);
+        }
+    } else if (warp < 12) {
+        // --------------------------------------------------- conversion
+        regs_dec<120>();
+        constexpr int UPR = DP / 16;       // 16-code units of a row
+        constexpr int NI = UPR;            // units of a thread: 128 rows of UPR over 128 threads
+        constexpr int RSTEP = 128 / UPR;   // rows between them
+        const int d = a.pool.d;
+        const int ct = tid - 256, u = ct % UPR, rb = ct / UPR;
+        const bool unit_on = u * 16 < d;
+        // units beyond head_dim repeat unit 0: their K meets zeros of Q, their V columns are not stored
+        const int8_t* kbase = a.pool.kc + (unit_on ? u * 16 : 0);
+        const int8_t* vbase = a.pool.vc + (unit_on ? u * 16 : 0);
+        // this thread's units of a tile, by the row offsets that warp 13 left
+        auto load = [&](uint4 (&x)[NI], const int8_t* base, uint32_t rows) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const uint2 o = lds64(rows + static_cast<uint32_t>(rb + i * RSTEP) * 8u);
+                x[i] = kv_ldg16(base + ((static_cast<int64_t>(o.y) << 32) | o.x));
+            }
+        };
+        auto rows_of = [&](int c) { return sbase + G::off_row + (c % kTcaRowSlots) * 2048u; };
+        bool ok = true;
+        int c = 0;
+        for (int sg = 0; ok; ++sg) {
+            ok = warp_wait(&seg_full[sg % kTcaSegSlots], sg / kTcaSegSlots, a.status);
+            if (!ok) break;
+            const volatile TcaSeg& g = segs[sg % kTcaSegSlots];
+            const int tiles = g.tiles;
+            if (tiles == 0) break;
+            uint4 kr[NI], vr[NI];
+            ok = warp_wait(&row_full[c % kTcaRowSlots], c / kTcaRowSlots, a.status);
+            if (!ok) break;
+            load(kr, kbase, rows_of(c));
+            load(vr, vbase, rows_of(c) + 1024u);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&row_free[c % kTcaRowSlots]);
 
-                // the unit's queries, once the products of the last one have read theirs
-                if (segs > 0) ok = warp_wait(q_free, segs - 1, a.status);
+            // the unit's queries, once the products of the last one have read theirs
+            if (sg > 0) ok = warp_wait(q_free, sg - 1, a.status);
+            if (!ok) break;
+            {
+                constexpr int CPR = DP / 8;  // 16-byte chunks of a row
+                const int rows = g.rows, row0 = g.row0, h = g.h;
+                const int64_t first = g.first;
+                const int qrows = rows - row0 > 128 ? 256 : 128;
+                const int ch = ct % CPR;
+#pragma unroll 4
+                for (int rr = ct / CPR; rr < qrows; rr += 128 / CPR) {
+                    const int row = row0 + rr;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < rows && ch * 8 < d) {
+                        const int tok = row / group;
+                        x = *reinterpret_cast<const uint4*>(
+                            a.q + (first + tok) * a.q_stride +
+                            static_cast<int64_t>(h * group + row - tok * group) * d + ch * 8);
+                    }
+                    const int rh = rr & 127;
+                    sts128(sbase + G::off_q + (rr >> 7) * G::tile + (ch >> 3) * 16384u + rh * 128u +
+                               (static_cast<uint32_t>((ch & 7) ^ (rh & 7)) << 4), x);
+                }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(q_full);
+                mbar_arrive(&seg_free[sg % kTcaSegSlots]);
+            }
+
+            for (int i = 0; i < tiles && ok; ++i, ++c) {
+                const int st = c & 1;
+                const uint32_t use = static_cast<uint32_t>(c >> 1);  // earlier uses of the stage
+                const bool more = i + 1 < tiles;
+                const int rs = (c + 1) % kTcaRowSlots;
+                if (use > 0) ok = warp_wait(&k_empty[st], use - 1, a.status);
                 if (!ok) break;
                 {
-                    constexpr int CPR = DP / 8;  // 16-byte chunks of a row
-                    const int qrows = g.both ? 256 : 128;
-                    const int ch = ct % CPR;
-#pragma unroll 4
-                    for (int rr = ct / CPR; rr < qrows; rr += 128 / CPR) {
-                        const int row = g.row0 + rr;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < g.rows && ch * 8 < pc.d) {
-                            const int tok = row / group;
-                            x = *reinterpret_cast<const uint4*>(
-                                a.q + (g.seq.first + tok) * a.q_stride +
-                                static_cast<int64_t>(w.h * group + row - tok * group) * pc.d + ch * 8);
-                        }
-                        const int rh = rr & 127;
-                        sts128(sbase + G::off_q + (rr >> 7) * G::tile + (ch >> 3) * 16384u + rh * 128u +
-                                   (static_cast<uint32_t>((ch & 7) ^ (rh & 7)) << 4), x);
-                    }
+                    const uint32_t tile = sbase + G::off_k + st * G::tile;
+#pragma unroll
+                    for (int q = 0; q < NI; ++q) tca_store16<BF16>(tile, rb + q * RSTEP, u, kr[q]);
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-
-                for (int i = 0; i < g.tiles && ok; ++i, ++c, j0 += kTcaKT) {
-                    const int st = c & 1;
-                    const uint32_t use = static_cast<uint32_t>(c >> 1);  // earlier uses of the stage
-                    const bool more = i + 1 < g.tiles;
-                    if (more) entries(j0 + kTcaKT);
-                    if (use > 0) {
-                        ok = warp_wait(&k_empty[st], use - 1, a.status) &&
-                             warp_wait(&sc_free[st], use - 1, a.status);
-                        if (!ok) break;
-                    }
-                    {
-                        const uint32_t tile = sbase + G::off_k + st * G::tile;
+                if (lane == 0) mbar_arrive(&k_full[st]);
+                if (more) {
+                    ok = warp_wait(&row_full[rs], (c + 1) / kTcaRowSlots, a.status);
+                    if (!ok) break;
+                    load(kr, kbase, rows_of(c + 1));
+                }
+                if (use > 0) ok = warp_wait(&v_empty[st], use - 1, a.status);
+                if (!ok) break;
+                {
+                    const uint32_t tile = sbase + G::off_v + st * G::tile;
 #pragma unroll
-                        for (int q = 0; q < NI; ++q) tca_store16<BF16>(tile, rb + q * RSTEP, u, kr[q]);
-                        float* sc = reinterpret_cast<float*>(smem + G::off_sc) + st * 384;
-                        const KvVScale v = kv_vscale(cache_value<BF16>(vs));
-                        const bool in = j0 + ct < g.seq.len;
-                        sc[ct] = cache_value<BF16>(ks) * a.scale_log2;
-                        sc[128 + ct] = in ? v.lg : 0.f;
-                        sc[256 + ct] = in ? v.inv : 0.f;
-                    }
-                    fence_async_shared();
+                    for (int q = 0; q < NI; ++q) tca_store16<false>(tile, rb + q * RSTEP, u, vr[q]);
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[st]);
+                if (more) {
+                    load(vr, vbase, rows_of(c + 1) + 1024u);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&k_full[st]);
+                    if (lane == 0) mbar_arrive(&row_free[rs]);
+                }
+            }
+        }
+    } else {
+        regs_dec<88>();
+        if (warp == 12 && lane == 0) {
+            // ---------------------------------------------- MMA issue
+            bool ok = true;
+            int c = 0;
+            uint32_t n[2] = {0, 0};
+            // A descriptor's low word is an address and grows by constants from step to
+            // step.  `opaque` keeps the compiler from computing the loop's 24 descriptors
+            // ahead of it and spilling them: with shared memory this full there is next to
+            // no L1, and each reload took 350 cycles (a tile 17,000 instead of 2,900).
+            auto opaque = [](uint32_t v) {
+                asm volatile("" : "+r"(v));
+                return v;
+            };
+            auto desc = [](uint32_t lo, uint32_t hi) {
+                uint64_t v;
+                asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+                return v;
+            };
+            const uint64_t kd = umma_desc_sw128_kmajor(sbase), nd = umma_desc_sw128_nmajor(sbase, 16384u);
+            const uint32_t klo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32);
+            const uint32_t nlo = static_cast<uint32_t>(nd), nhi = static_cast<uint32_t>(nd >> 32);
+            auto issue_s = [&](int half, int st) {
+                const uint32_t q = opaque(klo + ((G::off_q + half * G::tile) >> 4));
+                const uint32_t k = opaque(klo + ((G::off_k + st * G::tile) >> 4));
+                const uint32_t ds = opaque(tbase + half * 128);
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
+                    umma_f16_ss(ds, desc(q + off, khi), desc(k + off, khi), kIdescS, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&s_full[half]);
+            };
+            auto issue_pv = [&](int half, int st, bool add) {
+                const uint32_t v = opaque(nlo + ((G::off_v + st * G::tile) >> 4));
+                const uint32_t ds = opaque(tbase + kColO + half * DP), pa = opaque(tbase + half * 128);
+#pragma unroll
+                for (int kk = 0; kk < kTcaKT / 16; ++kk)
+                    umma_f16_ts(ds, pa + kk * 8, desc(v + kk * 128u, nhi), kIdescO,
+                                (add || kk > 0) ? 1u : 0u);
+                umma_commit(&pv_done[half]);
+            };
+            auto wait = [&](uint64_t* b, uint32_t ph) {
+                if (ok) ok = mbar_wait_bounded(b, ph & 1u, a.status, kWaitLimitNs);
+                tc_fence_after();
+                return ok;
+            };
+            for (int sg = 0; ok; ++sg) {
+                if (!wait(&seg_full[sg % kTcaSegSlots], sg / kTcaSegSlots)) break;
+                const volatile TcaSeg& g = segs[sg % kTcaSegSlots];
+                const int tiles = g.tiles;
+                if (tiles == 0) break;
+                const bool both = g.rows - g.row0 > 128;
+                mbar_arrive(&seg_free[sg % kTcaSegSlots]);
+                if (!wait(q_full, sg)) break;
+                if (!wait(&k_full[c & 1], c >> 1)) break;
+                issue_s(0, c & 1);
+                if (both) issue_s(1, c & 1);
+                umma_commit(&k_empty[c & 1]);
+                if (tiles == 1) umma_commit(q_free);
+                for (int i = 0; i < tiles; ++i, ++c) {
+                    const int st = c & 1, sn = (c + 1) & 1;
+                    const bool more = i + 1 < tiles;
+                    if (!wait(&v_full[st], c >> 1)) break;
+                    if (!wait(&p_ready[0], n[0]++)) break;
+                    issue_pv(0, st, i > 0);
                     if (more) {
-                        load(kr, pc.kc, pc.kc_page, j0 + kTcaKT);
-                        load_scales(j0 + kTcaKT);
+                        if (!wait(&k_full[sn], (c + 1) >> 1)) break;
+                        issue_s(0, sn);
                     }
-                    if (use > 0) {
-                        ok = warp_wait(&v_empty[st], use - 1, a.status);
-                        if (!ok) break;
+                    if (both) {
+                        if (!wait(&p_ready[1], n[1]++)) break;
+                        issue_pv(1, st, i > 0);
                     }
-                    {
-                        const uint32_t tile = sbase + G::off_v + st * G::tile;
+                    umma_commit(&v_empty[st]);
+                    if (more) {
+                        if (both) issue_s(1, sn);
+                        umma_commit(&k_empty[sn]);
+                        if (i + 2 == tiles) umma_commit(q_free);
+                    }
+                }
+            }
+            // every MMA has completed before tensor memory is released
+            umma_commit(drain);
+            mbar_wait_bounded(drain, 0, a.status, kWaitLimitNs);
+        } else if (warp == 13) {
+            // ------------------------------- row addresses and scales
+            const KvPool& pc = a.pool;
+            const int shift = (pc.ps & (pc.ps - 1)) == 0 ? 31 - __clz(pc.ps) : -1;
+            auto page_index = [&](int j) { return shift >= 0 ? j >> shift : j / pc.ps; };
+            bool ok = true;
+            int c = 0, sg = 0;
+            KvSeq seq{};
+            if (beg < end) seq = kv_seq(a.batch, w.b, a.status);
+            for (int64_t it = beg; ok; ++sg) {
+                // the next segment, or the end of the list
+                TcaSeg g{};
+                if (it < end) {
+                    int lo;
+                    const int n = kv_tiles(a.geom, seq, w.rt, &lo);
+                    const int64_t unit_beg = it - w.tile, unit_end = unit_beg + n;
+                    g.first = seq.first;
+                    g.past = seq.len - seq.n;
+                    g.rows = seq.n * group;
+                    g.row0 = w.rt * kTcaRows;
+                    g.h = w.h;
+                    g.tile0 = lo + w.tile;
+                    g.tiles = static_cast<int>(min(unit_end, end) - it);
+                    g.whole = it == unit_beg && it + g.tiles == unit_end;
+                    g.slot = it == beg ? 0 : 1;
+                    const int64_t fc = kv_owner(unit_beg, T, P);
+                    g.first_cta = static_cast<int>(fc);
+                    g.last_cta = static_cast<int>(kv_owner(unit_end - 1, T, P));
+                    g.first_slot = T * fc / P >= unit_beg ? 0 : 1;
+                }
+                const int gs = sg % kTcaSegSlots;
+                if (sg >= kTcaSegSlots) ok = warp_wait(&seg_free[gs], sg / kTcaSegSlots - 1, a.status);
+                if (!ok) break;
+                if (lane == 0) {
+                    segs[gs] = g;
+                    mbar_arrive(&seg_full[gs]);
+                }
+                __syncwarp();
+                if (g.tiles == 0) break;
+                int j = g.tile0 * kTcaKT + lane;
+                int32_t ent[4];
+                auto entries = [&](int jj) {
 #pragma unroll
-                        for (int q = 0; q < NI; ++q) tca_store16<false>(tile, rb + q * RSTEP, u, vr[q]);
+                    for (int e = 0; e < 4; ++e)
+                        ent[e] = jj + 32 * e < seq.len
+                                     ? kv_entry(a.batch, w.b, page_index(jj + 32 * e)) : 0;
+                };
+                entries(j);
+                for (int i = 0; i < g.tiles; ++i, ++c, j += kTcaKT) {
+                    const int rs = c % kTcaRowSlots, ss = c % kTcaScSlots;
+                    if (c >= kTcaRowSlots) ok = warp_wait(&row_free[rs], c / kTcaRowSlots - 1, a.status);
+                    if (!ok) break;
+                    uint16_t ks[4], vs[4];
+                    const uint32_t rows = sbase + G::off_row + rs * 2048u + lane * 8u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        int64_t ko = 0, vo = 0;  // no token: any row, its scores are masked
+                        ks[e] = vs[e] = 0;
+                        if (j + 32 * e < seq.len) {
+                            const int64_t page = kv_page(pc, ent[e], a.status);
+                            const int64_t row =
+                                kv_row(pc, w.h, j + 32 * e - page_index(j + 32 * e) * pc.ps);
+                            ko = page * pc.kc_page + row * pc.d;
+                            vo = page * pc.vc_page + row * pc.d;
+                            ks[e] = __ldg(pc.ks + page * pc.ks_page + row);
+                            vs[e] = __ldg(pc.vs + page * pc.vs_page + row);
+                        }
+                        sts64(rows + 256u * e, static_cast<uint64_t>(ko));
+                        sts64(rows + 1024u + 256u * e, static_cast<uint64_t>(vo));
                     }
-                    fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_full[st]);
-                    if (more) load(vr, pc.vc, pc.vc_page, j0 + kTcaKT);
+                    if (lane == 0) mbar_arrive(&row_full[rs]);
+                    if (i + 1 < g.tiles) entries(j + kTcaKT);
+                    if (c >= kTcaScSlots) ok = warp_wait(&sc_free[ss], c / kTcaScSlots - 1, a.status);
+                    if (!ok) break;
+                    float* sc = reinterpret_cast<float*>(smem + G::off_sc) + ss * 384 + lane;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const KvVScale v = kv_vscale(cache_value<BF16>(vs[e]));
+                        const bool in = j + 32 * e < seq.len;
+                        sc[32 * e] = cache_value<BF16>(ks[e]) * a.scale_log2;
+                        sc[128 + 32 * e] = in ? v.lg : 0.f;
+                        sc[256 + 32 * e] = in ? v.inv : 0.f;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[ss]);
                 }
                 it += g.tiles;
                 if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
-            }
-        } else {
-            regs_dec<40>();
-            if (warp == 12 && lane == 0) {
-                // ---------------------------------------------- MMA issue
-                bool ok = true;
-                int c = 0, segs = 0;
-                uint32_t n[2] = {0, 0};
-                auto issue_s = [&](int half, int st) {
-                    const uint32_t q = sbase + G::off_q + half * G::tile, k = sbase + G::off_k + st * G::tile;
-#pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
-                        umma_f16_ss(tbase + half * 128, umma_desc_sw128_kmajor(q + off),
-                                    umma_desc_sw128_kmajor(k + off), kIdescS, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&s_full[half]);
-                };
-                auto issue_pv = [&](int half, int st, bool add) {
-                    const uint32_t v = sbase + G::off_v + st * G::tile;
-#pragma unroll
-                    for (int kk = 0; kk < kTcaKT / 16; ++kk)
-                        umma_f16_ts(tbase + kColO + half * DP, tbase + half * 128 + kk * 8,
-                                    umma_desc_sw128_nmajor(v + kk * 2048u, 16384u), kIdescO,
-                                    (add || kk > 0) ? 1u : 0u);
-                    umma_commit(&pv_done[half]);
-                };
-                auto wait = [&](uint64_t* b, uint32_t ph) {
-                    if (ok) ok = mbar_wait_bounded(b, ph & 1u, a.status, kWaitLimitNs);
-                    tc_fence_after();
-                    return ok;
-                };
-                for (int64_t it = beg; it < end && ok; ++segs) {
-                    const Segment g = segment(it, w, seq);
-                    if (!wait(q_full, segs)) break;
-                    if (!wait(&k_full[c & 1], c >> 1)) break;
-                    issue_s(0, c & 1);
-                    if (g.both) issue_s(1, c & 1);
-                    umma_commit(&k_empty[c & 1]);
-                    if (g.tiles == 1) umma_commit(q_free);
-                    for (int i = 0; i < g.tiles; ++i, ++c) {
-                        const int st = c & 1, sn = (c + 1) & 1;
-                        const bool more = i + 1 < g.tiles;
-                        if (!wait(&v_full[st], c >> 1)) break;
-                        if (!wait(&p_ready[0], n[0]++)) break;
-                        issue_pv(0, st, i > 0);
-                        if (more) {
-                            if (!wait(&k_full[sn], (c + 1) >> 1)) break;
-                            issue_s(0, sn);
-                        }
-                        if (g.both) {
-                            if (!wait(&p_ready[1], n[1]++)) break;
-                            issue_pv(1, st, i > 0);
-                        }
-                        umma_commit(&v_empty[st]);
-                        if (more) {
-                            if (g.both) issue_s(1, sn);
-                            umma_commit(&k_empty[sn]);
-                            if (i + 2 == g.tiles) umma_commit(q_free);
-                        }
-                    }
-                    it += g.tiles;
-                    if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
-                }
-                // every MMA has completed before tensor memory is released
-                umma_commit(drain);
-                mbar_wait_bounded(drain, 0, a.status, kWaitLimitNs);
             }
         }
     }
