@@ -127,7 +127,8 @@ AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
 template <bool BF16, int DP, int NR>
 q4_status run_attention(const KvAttn& a, int64_t grid, cudaStream_t st) {
     constexpr size_t smem = kv_attention_smem<DP, NR>();
-    auto kernel = kv_attention_kernel<BF16, DP, NR>;
+    auto kernel = (a.pool.ps % 16) == 0 ? kv_attention_kernel<BF16, DP, NR, true>
+                                        : kv_attention_kernel<BF16, DP, NR, false>;
     if (!set_kernel_attrs(kernel, static_cast<int>(smem), false)) return Q4_ERR_CUDA;
     return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kKvWarps * 32), smem, 1, true,
                      st, a);

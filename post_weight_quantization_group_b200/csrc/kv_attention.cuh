@@ -94,7 +94,8 @@ __device__ __forceinline__ KvVScale kv_vscale(float sv) {
     KvVScale r;
     const float c = fmaxf(sv, 7.888609e-31f);  // 2^-100; a NaN becomes 2^-100 here ...
     r.lg = sv == sv ? __log2f(c) : sv;         // ... and stays in the exponent, where masks drop it
-    r.inv = fminf(__frcp_rn(c), 1.2676506e30f);
+    // within 1 ulp; c is normal and, as 1/127 of a finite value, below 2^121
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(c));
     return r;
 }
 
@@ -109,7 +110,9 @@ struct KvBlock {
 };
 
 // DP: head_dim padded to 64, 128 or 256.  NR: blocks of 8 rows (R = 8 NR).
-template <bool BF16, int DP, int NR>
+// P16: the page size is a multiple of 16, so a block of 16 tokens is in one
+// page and its rows follow one another; else every row looks up its own page.
+template <bool BF16, int DP, int NR, bool P16>
 __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     kv_attention_kernel(const __grid_constant__ KvAttn a) {
     constexpr int R = 8 * NR;
@@ -135,7 +138,17 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                              &beg, &end, &w);
     if (beg == end) return;
     KvSeq seq = kv_seq(a.batch, w.b, a.status);
-    const bool ps16 = (c.ps & 15) == 0;
+    const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;
+    auto page_index = [&](int j) { return shift >= 0 ? j >> shift : j / c.ps; };
+    // pieces beyond head_dim repeat piece 0: their K meets zeros of q, their V is not stored
+    int kcol[U], vcol[DP == 64 ? 1 : DP / 128];
+#pragma unroll
+    for (int u = 0; u < U; ++u) kcol[u] = u * 64 + t * 16 < d ? u * 64 + t * 16 : 0;
+#pragma unroll
+    for (int u = 0; u < (DP == 64 ? 1 : DP / 128); ++u) {
+        const int col = DP == 64 ? g * 8 : u * 128 + g * 16;
+        vcol[u] = col < d ? col : 0;
+    }
 
     int64_t it = beg;
     while (it < end) {
@@ -183,61 +196,58 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         }
 
         auto entry_of = [&](int j0) -> int32_t {
-            return ps16 && j0 < seq.len ? kv_entry(a.batch, w.b, j0 / c.ps) : 0;
+            return P16 && j0 < seq.len ? kv_entry(a.batch, w.b, page_index(j0)) : 0;
         };
-        // page and row of token j, which is in the 16-token block at j0
-        auto place = [&](int j, int j0, int64_t page16, int64_t* page, int64_t* row) {
-            if (ps16) {
-                *page = page16;
-                *row = kv_row(c, w.h, j0 % c.ps + (j - j0));
-            } else {
-                *page = kv_page(c, kv_entry(a.batch, w.b, j / c.ps), a.status);
-                *row = kv_row(c, w.h, j % c.ps);
-            }
+        // Where a block's rows are: offsets of token j0's row (P16), of a token's otherwise.
+        // Tokens behind the last one repeat it; the masks drop them.
+        struct Place {
+            int64_t kc, vc, ks, vs;
+        };
+        auto place = [&](int j, int32_t entry) {
+            const int64_t page = kv_page(c, entry, a.status);
+            const int64_t row = kv_row(c, w.h, j - page_index(j) * c.ps);
+            return Place{page * c.kc_page + row * d, page * c.vc_page + row * d, page * c.ks_page + row,
+                         page * c.vs_page + row};
+        };
+        auto row_of = [&](const Place& base, int j0, int r) {  // of token j0 + r
+            const int rr = min(r, seq.len - 1 - j0);
+            if constexpr (P16)
+                return Place{base.kc + rr * d, base.vc + rr * d, base.ks + rr, base.vs + rr};
+            else
+                return place(j0 + rr, kv_entry(a.batch, w.b, page_index(j0 + rr)));
         };
         KvBlock<DP> bk;
-        auto fetch_k = [&](int j0, int64_t page16) {
+        auto fetch_k = [&](int j0, const Place& base) {
+            if (j0 >= seq.len) return;  // nothing of the block is visible either
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = j0 + g + 8 * e;
-                const bool in = j < seq.len;
-                int64_t page = 0, row = 0;
-                if (in) place(j, j0, page16, &page, &row);
-                const int8_t* p = c.kc + page * c.kc_page + row * d;
+                const int8_t* p = c.kc + row_of(base, j0, g + 8 * e).kc;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    bk.k[e][u] = in && u * 64 + t * 16 < d ? kv_ldg16(p + u * 64 + t * 16)
-                                                           : make_uint4(0u, 0u, 0u, 0u);
+                for (int u = 0; u < U; ++u) bk.k[e][u] = kv_ldg16(p + kcol[u]);
             }
         };
-        auto fetch_scales = [&](int j0, int64_t page16) {
+        auto fetch_scales = [&](int j0, const Place& base) {
+            if (j0 >= seq.len) return;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = j0 + g + 8 * e;
-                const bool in = j < seq.len;
-                int64_t page = 0, row = 0;
-                if (in) place(j, j0, page16, &page, &row);
-                bk.ks[e] = in ? __ldg(c.ks + page * c.ks_page + row) : uint16_t(0);
-                bk.vs[e] = in ? __ldg(c.vs + page * c.vs_page + row) : uint16_t(0);
+                const Place r = row_of(base, j0, g + 8 * e);
+                bk.ks[e] = __ldg(c.ks + r.ks);
+                bk.vs[e] = __ldg(c.vs + r.vs);
             }
         };
-        auto fetch_v = [&](int j0, int64_t page16) {
+        auto fetch_v = [&](int j0, const Place& base) {
+            if (j0 >= seq.len) return;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int j = j0 + 2 * t + (e & 1) + 8 * (e >> 1);
-                const bool in = j < seq.len;
-                int64_t page = 0, row = 0;
-                if (in) place(j, j0, page16, &page, &row);
-                const int8_t* p = c.vc + page * c.vc_page + row * d;
+                const int8_t* p = c.vc + row_of(base, j0, 2 * t + (e & 1) + 8 * (e >> 1)).vc;
                 if constexpr (DP == 64) {
-                    const uint2 x = in && g * 8 < d ? kv_ldg8(p + g * 8) : make_uint2(0u, 0u);
+                    const uint2 x = kv_ldg8(p + vcol[0]);
                     bk.v[e][0] = x.x;
                     bk.v[e][1] = x.y;
                 } else {
 #pragma unroll
                     for (int u = 0; u < DP / 128; ++u) {
-                        const uint4 x = in && u * 128 + g * 16 < d ? kv_ldg16(p + u * 128 + g * 16)
-                                                                   : make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 x = kv_ldg16(p + vcol[u]);
                         bk.v[e][4 * u] = x.x;
                         bk.v[e][4 * u + 1] = x.y;
                         bk.v[e][4 * u + 2] = x.z;
@@ -252,21 +262,24 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         // other half of a step (and the 16 warps of an SM hold 64 KB between them)
         // without a second set of registers.
         int j0 = (tile_lo + w.tile) * kKvTile + warp * 16;
-        int64_t page_next = kv_page(c, entry_of(j0), a.status);
+        auto base_of = [&](int j0, int32_t entry) {
+            return P16 && j0 < seq.len ? place(j0, entry) : Place{0, 0, 0, 0};
+        };
+        Place nb = base_of(j0, entry_of(j0));
         int32_t entry_next = nseg > 1 ? entry_of(j0 + kKvTile) : 0;
-        fetch_k(j0, page_next);
-        fetch_scales(j0, page_next);
-        fetch_v(j0, page_next);
+        fetch_k(j0, nb);
+        fetch_scales(j0, nb);
+        fetch_v(j0, nb);
         for (int s = 0; s < nseg; ++s, j0 += kKvTile) {
             const bool more = s + 1 < nseg;
-            if (more) page_next = kv_page(c, entry_next, a.status);
+            if (more) nb = base_of(j0 + kKvTile, entry_next);
             if (s + 2 < nseg) entry_next = entry_of(j0 + 2 * kKvTile);
             // nothing of this block is visible to any row: at the ends of a unit's range
             if (j0 > at_max || (a.geom.window && j0 + 15 <= at_min - a.geom.window)) {
                 if (more) {
-                    fetch_k(j0 + kKvTile, page_next);
-                    fetch_scales(j0 + kKvTile, page_next);
-                    fetch_v(j0 + kKvTile, page_next);
+                    fetch_k(j0 + kKvTile, nb);
+                    fetch_scales(j0 + kKvTile, nb);
+                    fetch_v(j0 + kKvTile, nb);
                 }
                 continue;
             }
@@ -288,13 +301,13 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         mma_16816<BF16>(x[n], af, qf[n][u * 4 + i].x, qf[n][u * 4 + i].y);
                 }
             }
-            if (more) fetch_k(j0 + kKvTile, page_next);
+            if (more) fetch_k(j0 + kKvTile, nb);
             // scores in log2, with the V scale; masks
             const float sk0 = cache_value<BF16>(bk.ks[0]) * a.scale_log2;
             const float sk1 = cache_value<BF16>(bk.ks[1]) * a.scale_log2;
             const KvVScale v0 = kv_vscale(cache_value<BF16>(bk.vs[0]));
             const KvVScale v1 = kv_vscale(cache_value<BF16>(bk.vs[1]));
-            if (more) fetch_scales(j0 + kKvTile, page_next);
+            if (more) fetch_scales(j0 + kKvTile, nb);
             const bool open = j0 + 15 <= at_min && (!a.geom.window || j0 > at_max - a.geom.window);
             bool grow = false;
 #pragma unroll
@@ -325,7 +338,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-                        mx = fmaxf(mx, m[n][e]);
+                        // a row of its own: what other rows of the warp do leaves it alone
+                        mx = mx > m[n][e] + kKvLazy ? mx : m[n][e];
                         f[e] = kv_exp2(m[n][e] - mx);
                         m[n][e] = mx;
                         l[n][e] *= f[e];
@@ -367,7 +381,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         mma_16816<false>(o[2 * i + hw][n], af, pb[n][0], pb[n][1]);
                 }
             }
-            if (more) fetch_v(j0 + kKvTile, page_next);
+            if (more) fetch_v(j0 + kKvTile, nb);
         }
 
         // ------------------------------------------- join of the CTA's warps

@@ -63,7 +63,9 @@ struct TcaGeom {
     static constexpr uint32_t off_row = off_sc + kTcaScSlots * 3 * 128 * 4;  // K, V offsets [128]
     static constexpr uint32_t off_bar = off_row + kTcaRowSlots * 2 * 128 * 8;
     static constexpr uint32_t off_seg = off_bar + 512;
-    static constexpr uint32_t total = off_seg + kTcaSegSlots * 64 + 1024;
+    static constexpr uint32_t off_at = off_seg + kTcaSegSlots * 64;  // last visible token, per row
+    static constexpr uint32_t off_one = off_at + 1024;               // 128 ones, 128 zeros
+    static constexpr uint32_t total = off_one + 1024 + 1024;
 };
 
 // Packed fp32 pairs: one instruction for both.
@@ -98,8 +100,7 @@ __device__ __forceinline__ uint64_t lds_f2(uint32_t addr) {
 }
 
 // Sixteen codes of token `row`, unit `u` of its DP / 16, as 16-bit floats into
-// a tile.  The second half of a 128-element row stores its chunks in the other
-// order, so that eight lanes of a row hit eight different 16-byte columns.
+// a tile.
 template <bool BF16>
 __device__ __forceinline__ void tca_store16(uint32_t tile, int row, int u, const uint4& raw) {
     uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -116,11 +117,9 @@ __device__ __forceinline__ void tca_store16(uint32_t tile, int row, int u, const
         }
     }
     const uint32_t base = tile + (u >> 2) * 16384u + static_cast<uint32_t>(row) * 128u;
-    const uint32_t c = static_cast<uint32_t>(u & 3) * 2, x = static_cast<uint32_t>(row & 7);
-    const bool odd = (u >> 2) & 1;
-    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-    sts128(base + (((odd ? c + 1 : c) ^ x) << 4), odd ? hi : lo);
-    sts128(base + (((odd ? c : c + 1) ^ x) << 4), odd ? lo : hi);
+    const uint32_t at = (static_cast<uint32_t>(u & 3) * 2u ^ static_cast<uint32_t>(row & 7)) << 4;
+    sts128(base + at, make_uint4(o[0], o[1], o[2], o[3]));
+    sts128(base + (at ^ 16u), make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 // A warp's bounded wait, with one outcome for all of its lanes: a wait that
@@ -195,6 +194,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
         mbar_init(drain, 1);
         fence_mbarrier_init_cluster();
     }
+    if (tid < 256) reinterpret_cast<float*>(smem + G::off_one)[tid] = tid < 128 ? 1.f : 0.f;
     if (warp == 12) tmem_alloc(tbase_s, 512);
     tc_fence_before();
     __syncthreads();
@@ -208,10 +208,14 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
     kv_locate<kTcaThreads>(a.batch, a.geom, blockIdx.x, gridDim.x, 1, a.status, &s_loc, &T, &P, &beg,
                            &end, &w);
     const int group = a.geom.group, window = a.geom.window;
+    // a value the compiler cannot compute ahead of its use
+    auto opaque = [](uint32_t v) {
+        asm volatile("" : "+r"(v));
+        return v;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------ softmax
-        regs_inc<152>();
         const int half = warp >> 2;
         const uint32_t tl = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t ts = tl + half * 128, to = tl + kColO + half * DP;
@@ -220,6 +224,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
         uint32_t n = 0;   // tiles of this half so far
         bool ok = true;
         uint32_t parts = 0;  // shared units so far
+        const uint32_t s_at = sbase + G::off_at + warp * 128u;
         // the value of row `lane` of the warp, from the quad that holds it as its k-th
         auto by_lane = [&](const float (&v)[4]) {
             const int src = (lane & 7) * 4;
@@ -239,19 +244,16 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             if (tiles == 0) break;
             const bool active = half == 0 || g.rows - g.row0 > 128;
             const bool warp_live = g.row0 + r - lane < g.rows;
-            // last visible token of this thread's rows 8 k + lane / 4
-            int at[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int rr = g.row0 + r - lane + 8 * k + (lane >> 2);
-                at[k] = rr < g.rows ? g.past + rr / group : -1;
-            }
+            // the rows' last visible tokens, read back where a tile needs masks
+            __syncwarp();
+            sts32(s_at + (lane << 2), g.row0 + r < g.rows ? g.past + (g.row0 + r) / group : -1);
+            __syncwarp();
             // a tile at j0 is open to every row of the half if j0 <= open_hi, > open_lo
             const int open_hi = g.past + (g.row0 + half * 128) / group - (kTcaKT - 1);
             const int open_lo =
                 window ? g.past + (min(g.row0 + half * 128 + 128, g.rows) - 1) / group - window : -1;
             float m[4] = {kKvNone, kKvNone, kKvNone, kKvNone};
-            uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+            float l[4] = {0.f, 0.f, 0.f, 0.f};
             for (int i = 0; i < tiles && ok; ++i, ++c) {
                 const int slot = c % kTcaScSlots;
                 if (active) ok = warp_wait(&s_full[half], n, a.status);
@@ -269,125 +271,154 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 tc_fence_after();
                 const uint32_t sc = sbase + G::off_sc + slot * 1536u + (lane & 3) * 8u;
                 const int j0 = (tile0 + i) * kTcaKT;
-                const bool open = j0 <= open_hi && j0 > open_lo;
-                // S of columns 32 q .. 32 q + 31: the warp's lanes 0-15, then 16-31
-                auto read_s = [&](int q, uint32_t (&v)[32]) {
-                    tmem_ld_frag32(ts + 32 * q, v);
-                    tmem_ld_frag32(ts + 32 * q + (16u << 16), v + 16);
+                // S of columns 16 q .. 16 q + 15: the warp's lanes 0-15, then 16-31
+                auto read_s = [&](int q, uint32_t (&v)[16]) {
+                    tmem_ld_frag16(ts + 16 * q, v);
+                    tmem_ld_frag16(ts + 16 * q + (16u << 16), v + 8);
                 };
-                // x = S sk + lg, masked: x[8 e + 2 y + z] of row 8 (2 e + z) + lane / 4 and the
-                // columns 32 q + 8 y + 2 (lane % 4), + 1
-                auto scores = [&](int q, const uint32_t (&v)[32], uint64_t (&x)[16]) {
+                // A tile that some row does not see whole: its scores are scaled and masked in
+                // tensor memory first, and the pass below finds scales of one and zero.
+                uint32_t scx = sc;
+                if (!(j0 <= open_hi && j0 > open_lo)) {
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t v[16];
+                        read_s(q, v);
+                        tmem_wait_ld_for(v);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint64_t sk = lds_f2(sc + 128 * q + 32 * y);
-                        const uint64_t lg = lds_f2(sc + 512 + 128 * q + 32 * y);
+                        for (int y = 0; y < 2; ++y) {
+                            const uint64_t sk = lds_f2(sc + 64 * q + 32 * y);
+                            const uint64_t lg = lds_f2(sc + 512 + 64 * q + 32 * y);
+                            const int col = j0 + 16 * q + 8 * y + 2 * (lane & 3);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t* w2 = v + 16 * e + 4 * y + 2 * z;
-                                x[8 * e + 2 * y + z] = f2_fma(
-                                    f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])), sk, lg);
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t* w2 = v + 8 * (k >> 1) + 4 * y + 2 * (k & 1);
+                                const int top = static_cast<int>(lds32(s_at + ((8 * k + (lane >> 2)) << 2)));
+                                const int low = window ? top - window : INT32_MIN;
+                                float u, t;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])), sk, lg),
+                                          u, t);
+                                if (col > top || col <= low) u = -INFINITY;
+                                if (col + 1 > top || col + 1 <= low) t = -INFINITY;
+                                w2[0] = __float_as_uint(u);
+                                w2[1] = __float_as_uint(t);
                             }
-                    }
-                    if (!open) {
-                        const int c0 = j0 + 32 * q + 2 * (lane & 3);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int col = c0 + 8 * ((e >> 1) & 3), top = at[2 * (e >> 3) + (e & 1)];
-                            float u, t;
-                            f2_unpack(x[e], u, t);
-                            if (col > top || (window && col <= top - window)) u = -INFINITY;
-                            if (col + 1 > top || (window && col + 1 <= top - window)) t = -INFINITY;
-                            x[e] = f2_pack(u, t);
                         }
+                        tmem_st_frag16w(ts + 16 * q, v);
+                        tmem_st_frag16w(ts + 16 * q + (16u << 16), v + 8);
                     }
-                };
-                uint32_t sv[2][32];
-                float mx[4] = {kKvNone, kKvNone, kKvNone, kKvNone};
-                // two passes over S (maxima, then weights), each chunk read one ahead: the
-                // whole row in registers would spill, and there is next to no L1 to spill to
+                    tmem_wait_st();
+                    scx = sbase + G::off_one + (lane & 3) * 8u;
+                }
+                // One pass, 16 columns at a time, the next ones' S on its way: x = S sk + lg,
+                // p' = 2^(x - m) with the maximum known so far, their sum with 1 / sv into l. The
+                // packed p' of columns 16 q .. go over columns 8 q .. of S, which have been read.
+                // A chunk whose maximum is more than kKvLazy above m (rare after a segment's
+                // first tile) raises m first and rescales what has been added with the old one:
+                // l, O and this tile's earlier weights (a second rounding to fp16 for those).
+                uint64_t lx[4], neg_m[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    lx[k] = f2_pack(l[k], 0.f);
+                    neg_m[k] = f2_pack(-m[k], -m[k]);
+                }
+                uint32_t sv[2][16];
                 read_s(0, sv[0]);
 #pragma unroll 1
-                for (int q2 = 0; q2 < 4; q2 += 2) {
+                for (int q2 = 0; q2 < 8; q2 += 2) {
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const int q = q2 + h2;
-                        tmem_wait_ld();
-                        read_s((q + 1) & 3, sv[h2 ^ 1]);  // after the last: chunk 0 for the second pass
-                        uint64_t x[16];
-                        scores(q, sv[h2], x);
+                    for (int z = 0; z < 2; ++z) {
+                        const int q = q2 + z;
+                        uint32_t(&v)[16] = sv[z];
+                        tmem_wait_ld_for(v);
+                        if (z == 0 || q2 < 6) read_s(q + 1, sv[z ^ 1]);
+                        uint64_t x[8];
+                        float mx[4];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float u, t;
-                            f2_unpack(x[e], u, t);
-                            float& mr = mx[2 * (e >> 3) + (e & 1)];
-                            mr = f_max3(mr, u, t);
+                        for (int y = 0; y < 2; ++y) {
+                            const uint64_t sk = lds_f2(scx + 64 * q + 32 * y);
+                            const uint64_t lg = lds_f2(scx + 512 + 64 * q + 32 * y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t* w2 = v + 8 * (k >> 1) + 4 * y + 2 * (k & 1);
+                                x[4 * y + k] = f2_fma(f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])),
+                                                      sk, lg);
+                            }
                         }
-                    }
-                }
-                bool grow = false;
+                        bool grow = false;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) grow |= mx[k] > m[k] + kKvLazy;
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-                    float f[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
-                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
-                        const float mn = fmaxf(m[k], mx[k]);
-                        f[k] = kv_exp2(m[k] - mn);
-                        m[k] = mn;
-                        l2[k] = f2_fma(l2[k], f2_pack(f[k], f[k]), 0ull);
-                    }
-                    if (i > 0) {
-                        const float fr = by_lane(f);
-                        ok = warp_wait(&pv_done[half], n - 1, a.status);
-                        tc_fence_after();
-                        tmem_wait_ld();
-#pragma unroll 1
-                        for (int q = 0; q < DP / 8; ++q) {
-                            uint32_t o[8];
-                            tmem_ld8(to + 8 * q, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
-                            tmem_st8(to + 8 * q, o);
+                        for (int k = 0; k < 4; ++k) {
+                            float u0, t0, u1, t1;
+                            f2_unpack(x[k], u0, t0);
+                            f2_unpack(x[4 + k], u1, t1);
+                            mx[k] = fmaxf(f_max3(u0, t0, u1), t1);
+                            grow |= mx[k] > m[k] + kKvLazy;
                         }
-                    }
-                }
-                // p' of 32 columns go over the S columns 16 q .. 16 q + 15, which have been read
+                        if (__any_sync(0xFFFFFFFFu, grow)) {
+                            float f[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
+                                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
+                                // each row of its own: what the warp's other rows do leaves it alone
+                                const float mn = mx[k] > m[k] + kKvLazy ? mx[k] : m[k];
+                                f[k] = kv_exp2(m[k] - mn);
+                                m[k] = mn;
+                                lx[k] = f2_fma(lx[k], f2_pack(f[k], f[k]), 0ull);
+                                neg_m[k] = f2_pack(-mn, -mn);
+                            }
+                            const float fr = by_lane(f);
+                            if (i > 0) {
+                                ok = warp_wait(&pv_done[half], n - 1, a.status) && ok;
+                                tc_fence_after();
 #pragma unroll 1
-                for (int q2 = 0; q2 < 4; q2 += 2) {
+                                for (int o8 = 0; o8 < DP / 8; ++o8) {
+                                    uint32_t o[8];
+                                    tmem_ld8(to + 8 * o8, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const int q = q2 + h2;
-                        tmem_wait_ld();
-                        if (q < 3) read_s(q + 1, sv[h2 ^ 1]);
-                        uint64_t x[16];
-                        scores(q, sv[h2], x);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint64_t inv = lds_f2(sc + 1024 + 128 * q + 32 * y);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    const int k = 2 * e + z;
-                                    float u, t;
-                                    f2_unpack(f2_add(x[8 * e + 2 * y + z], f2_pack(-m[k], -m[k])), u, t);
-                                    u = kv_exp2(u);
-                                    t = kv_exp2(t);
-                                    l2[k] = f2_fma(f2_pack(u, t), inv, l2[k]);
-                                    p[8 * e + 2 * y + z] = kv_pack_f16(u, t);
+                                    for (int e = 0; e < 8; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+                                    tmem_st8(to + 8 * o8, o);
                                 }
+                            }
+                            tmem_wait_st();  // the earlier chunks' weights
+#pragma unroll 1
+                            for (int o8 = 0; o8 < q; ++o8) {
+                                uint32_t o[8];
+                                tmem_ld8(ts + 8 * o8, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const __half2 h2 = *reinterpret_cast<__half2*>(&o[e]);
+                                    o[e] = kv_pack_f16(__low2float(h2) * fr, __high2float(h2) * fr);
+                                }
+                                tmem_st8(ts + 8 * o8, o);
+                            }
                         }
-                        tmem_st_frag16(ts + 16 * q, p);
-                        tmem_st_frag16(ts + 16 * q + (16u << 16), p + 8);
+                        uint32_t p[8];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint64_t inv = lds_f2(sc + 1024 + 64 * q + 32 * y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float u, t;
+                                f2_unpack(f2_add(x[4 * y + k], neg_m[k]), u, t);
+                                u = kv_exp2(u);
+                                t = kv_exp2(t);
+                                lx[k] = f2_fma(f2_pack(u, t), inv, lx[k]);
+                                p[4 * (k >> 1) + 2 * y + (k & 1)] = kv_pack_f16(u, t);
+                            }
+                        }
+                        tmem_st_pairs8(ts + 8 * q, p);
+                        tmem_st_pairs8(ts + 8 * q + (16u << 16), p + 4);
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float u, t;
+                    f2_unpack(lx[k], u, t);
+                    l[k] = u + t;
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -398,20 +429,12 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 }
                 ++n;
             }
-            float ms = 0.f, l = 0.f;  // this lane's row's
-            {
-                float ls[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float u, t;
-                    f2_unpack(l2[k], u, t);
-                    ls[k] = u + t;
-                    ls[k] += __shfl_xor_sync(0xFFFFFFFFu, ls[k], 1);
-                    ls[k] += __shfl_xor_sync(0xFFFFFFFFu, ls[k], 2);
-                }
-                l = by_lane(ls);
-                ms = by_lane(m);
+            for (int k = 0; k < 4; ++k) {
+                l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
             }
+            const float ls = by_lane(l), ms = by_lane(m);  // this lane's row's
             // ------------------------------------- end of the segment
             const bool whole = g.whole != 0;
             const int row = g.row0 + r, tok = row / group;
@@ -439,12 +462,12 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 // a slot: m [256], l [256], O [DP][256] (a column of rows together)
                 float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + g.slot) * SLOT;
                 if (whole) {
-                    if (live) store_lse(ms, l);
+                    if (live) store_lse(ms, ls);
                 } else {
                     __stcg(part + r, ms);
-                    __stcg(part + kTcaRows + r, l);
+                    __stcg(part + kTcaRows + r, ls);
                 }
-                const float inv = inverse(l);
+                const float inv = inverse(ls);
 #pragma unroll 1
                 for (int q = 0; q < DP / 16; ++q) {
                     uint32_t o[16];
@@ -511,12 +534,13 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
         }
     } else if (warp < 12) {
         // --------------------------------------------------- conversion
-        regs_dec<120>();
         constexpr int UPR = DP / 16;       // 16-code units of a row
         constexpr int NI = UPR;            // units of a thread: 128 rows of UPR over 128 threads
         constexpr int RSTEP = 128 / UPR;   // rows between them
         const int d = a.pool.d;
-        const int ct = tid - 256, u = ct % UPR, rb = ct / UPR;
+        // The eight lanes of a 128-element row take its first half from row rb and the
+        // second from its neighbour, so that their stores hit eight different columns.
+        const int ct = tid - 256, u = ct % UPR, rb = (ct / UPR) ^ (u >> 2);
         const bool unit_on = u * 16 < d;
         // units beyond head_dim repeat unit 0: their K meets zeros of Q, their V columns are not stored
         const int8_t* kbase = a.pool.kc + (unit_on ? u * 16 : 0);
@@ -615,7 +639,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             }
         }
     } else {
-        regs_dec<88>();
         if (warp == 12 && lane == 0) {
             // ---------------------------------------------- MMA issue
             bool ok = true;
@@ -625,10 +648,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             // step.  `opaque` keeps the compiler from computing the loop's 24 descriptors
             // ahead of it and spilling them: with shared memory this full there is next to
             // no L1, and each reload took 350 cycles (a tile 17,000 instead of 2,900).
-            auto opaque = [](uint32_t v) {
-                asm volatile("" : "+r"(v));
-                return v;
-            };
             auto desc = [](uint32_t lo, uint32_t hi) {
                 uint64_t v;
                 asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));

@@ -63,26 +63,42 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr)
         : "memory");
 }
-// Sixteen lanes (taddr's and the 15 after it) x 32 columns in the layout of MMA
+// Sixteen lanes (taddr's and the 15 after it) x 16 columns in the layout of MMA
 // accumulators: of the i-th 8 columns, v[4 i], v[4 i + 1] are columns 2 (lane % 4),
 // + 1 of lane lane / 4, and v[4 i + 2], v[4 i + 3] the same of lane lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t* v) {
+// No memory clobber: the values are tied to the wait by tmem_wait_ld_for instead, so that
+// the compiler may schedule other loads around both.
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* v) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr)
-        : "memory");
+          "=r"(v[7])
+        : "r"(taddr));
 }
-// Sixteen lanes x 16 columns of packed pairs in the same layout: v[2 i] is column
-// 4 i + lane % 4 of lane lane / 4, v[2 i + 1] of lane lane / 4 + 8.
-__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t* v) {
+__device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                   "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                   "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+__device__ __forceinline__ void tmem_st_frag16w(uint32_t taddr, const uint32_t* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
+}
+// Sixteen lanes x 8 columns of packed pairs in the same layout: v[2 i] is column
+// 4 i + lane % 4 of lane lane / 4, v[2 i + 1] of lane lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_pairs8(uint32_t taddr, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x2.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -169,17 +185,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 // core's reads that are ordered after it.
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// This warpgroup's registers per thread from here on (a multiple of 8); all of
-// its warps execute it.
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 }  // namespace q4dev
