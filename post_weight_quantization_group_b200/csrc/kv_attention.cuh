@@ -12,15 +12,22 @@
 // range; the denominator adds the unrounded fp32 p'.  V scales below 2^-100
 // are taken as 2^-100 (an absolute error below 2^-93).
 //
-// Bound by the cache bytes read once from HBM.  Nothing of a cached row goes
-// through shared memory: with the products transposed, S^T = K q^T and
-// O^T = V^T P^T (mma.sync m16n8k16), a thread's fragment of K is 16-byte
-// pieces of a row and of V 16-byte pieces of four rows, loaded straight to
-// registers one block of 16 tokens ahead, because the order of head_dim
-// inside the dot product and of head_dim in the accumulator's rows is free.
-// The eight query rows of an MMA's N are one KV head's group at a decode step
-// (the tensor pipe is far from a bound here: 8 warps issue 16 MMAs per 4 KB).
-// P^T comes out of S^T's accumulator by one movmatrix per 8 tokens.
+// Bound by the cache bytes read once from HBM.  A warp works alone on blocks
+// of 16 tokens: cp.async brings a block's codes into its own ring of shared
+// memory kKvStages ahead (128 KB in flight per SM), with no barrier but the
+// warp's.  The products are transposed, S^T = K q^T and O^T = V^T P^T
+// (mma.sync m16n8k16), so that a thread's fragment of K is 16-byte pieces of
+// a row and of V 16-byte pieces of four rows, because the order of head_dim
+// inside the dot product and of head_dim in the accumulator's rows is free;
+// the ring's pieces are XOR-ed with their row so that both reads are free of
+// bank conflicts.  The eight query rows of an MMA's N are one KV head's group
+// at a decode step.  P^T comes out of S^T's accumulator by one movmatrix per
+// 8 tokens.
+//
+// Codes become fp16 for both products (5 instructions for 4 codes; bf16 would
+// take 8): the queries are scaled by a power of two per row into fp16's range
+// first, which is exact for every element above 2^-31 of the row's largest,
+// and below that within 2^-40 of it: finer than the fp32 sums.
 //
 // Work split: kv_paged.cuh (equal ranges of 128-token tiles over the CTAs; a
 // warp takes 16 tokens of each tile).  The warps of a CTA keep their own
@@ -65,11 +72,6 @@ __device__ __forceinline__ uint4 kv_ldg16(const void* p) {
                  : "l"(p));
     return v;
 }
-__device__ __forceinline__ uint2 kv_ldg8(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ float kv_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -79,6 +81,14 @@ __device__ __forceinline__ uint32_t kv_pack_f16(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+// Two codes of a word whose bytes have had 0x80 added, bytes 0, 1 or 2, 3, as exact fp16:
+// a byte under 0x64 is 1024 + (code + 128).
+__device__ __forceinline__ uint32_t kv_codes01(uint32_t w) {
+    return sub2<false>(prmt(w, 0x64u, 0x4140u), 0x64806480u);
+}
+__device__ __forceinline__ uint32_t kv_codes23(uint32_t w) {
+    return sub2<false>(prmt(w, 0x64u, 0x4342u), 0x64806480u);
 }
 __device__ __forceinline__ uint32_t kv_transpose8x8(uint32_t v) {
     uint32_t d;
@@ -99,15 +109,38 @@ __device__ __forceinline__ KvVScale kv_vscale(float sv) {
     return r;
 }
 
-// A block of 16 cached tokens as one thread holds it.
+// A warp's ring in shared memory: stages of a block's K and V codes, then of its
+// tokens' scales (sk, log2 sv, 1 / sv).
 template <int DP>
-struct KvBlock {
-    static constexpr int U = DP / 64;                 // 64-byte pieces of a K row
-    static constexpr int VW = DP / 32;                // words of a thread's piece of a V row
-    uint4 k[2][U];                                    // rows g, g + 8
-    uint32_t v[4][VW];                                // rows 2t, 2t + 1, 2t + 8, 2t + 9
-    uint16_t ks[2], vs[2];                            // scales of tokens g, g + 8
+struct KvRing {
+    static constexpr int stages = DP == 64 ? 5 : 3;
+    static constexpr uint32_t half = 16 * DP;  // bytes of a block's K, of its V
+    static constexpr uint32_t off_sc = stages * 2 * half;
+    static constexpr uint32_t total = off_sc + stages * 3 * 16 * 4;
+    static constexpr int lanes = DP / 16;        // lanes of a row, 16 bytes each
+    static constexpr int rows = 32 / lanes;      // rows of one cp.async of the warp
+    static constexpr int copies = 16 / rows;
+    // Byte offset of 16-byte piece p of token r.  K is read by lanes (two rows, four
+    // pieces) at a time, V by (four even or odd rows, two pieces).
+    static __device__ __forceinline__ uint32_t k_at(int r, int p) {
+        return DP == 64 ? r * 64 + p * 16 : r * DP + ((p ^ ((r & 1) << 2)) << 4);
+    }
+    static __device__ __forceinline__ uint32_t v_at(int r, int p) {
+        if constexpr (DP == 64)
+            return ((r & ~3) | ((r & 1) << 1) | ((r >> 1) & 1)) * 64 + ((p ^ ((r >> 1) & 2)) << 4);
+        else
+            return r * DP + ((p ^ (r & 6)) << 4);
+    }
 };
+
+__device__ __forceinline__ void kv_cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void kv_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void kv_cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // DP: head_dim padded to 64, 128 or 256.  NR: blocks of 8 rows (R = 8 NR).
 // P16: the page size is a multiple of 16, so a block of 16 tokens is in one
@@ -116,9 +149,11 @@ template <bool BF16, int DP, int NR, bool P16>
 __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     kv_attention_kernel(const __grid_constant__ KvAttn a) {
     constexpr int R = 8 * NR;
-    constexpr int U = DP / 64, VW = DP / 32, MT = DP / 16;
+    constexpr int U = DP / 64, MT = DP / 16;
     constexpr int ROW = DP + 8;  // padded row of the join buffer (floats): rows 2t apart by 16 banks
-    extern __shared__ float smem[];
+    using Ring = KvRing<DP>;
+    extern __shared__ __align__(128) float smem[];
+    // the warps' rings; at the end of a segment the same memory joins their parts
     float* s_o = smem;                                // [warps][R][ROW]
     float* s_m = smem + kKvWarps * R * ROW;           // [warps][R]
     float* s_l = s_m + kKvWarps * R;                  // [warps][R]
@@ -140,15 +175,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     KvSeq seq = kv_seq(a.batch, w.b, a.status);
     const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;
     auto page_index = [&](int j) { return shift >= 0 ? j >> shift : j / c.ps; };
-    // pieces beyond head_dim repeat piece 0: their K meets zeros of q, their V is not stored
-    int kcol[U], vcol[DP == 64 ? 1 : DP / 128];
-#pragma unroll
-    for (int u = 0; u < U; ++u) kcol[u] = u * 64 + t * 16 < d ? u * 64 + t * 16 : 0;
-#pragma unroll
-    for (int u = 0; u < (DP == 64 ? 1 : DP / 128); ++u) {
-        const int col = DP == 64 ? g * 8 : u * 128 + g * 16;
-        vcol[u] = col < d ? col : 0;
-    }
+    const uint32_t ring = smem_u32(smem) + warp * Ring::total;
+    const bool same = c.kc_page == c.vc_page && c.ks_page == c.vs_page;
+    // this lane's part of a copy: row crow (and every Ring::rows after it), piece cp; pieces
+    // beyond head_dim repeat piece 0: their K meets zeros of q, their V is not stored
+    const int crow = lane / Ring::lanes, cp = lane % Ring::lanes;
+    const int ccol = cp * 16 < d ? cp * 16 : 0;
 
     int64_t it = beg;
     while (it < end) {
@@ -159,8 +191,10 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         const int rows = seq.n * a.geom.group;
         const int row0 = w.rt * R;
 
-        // query fragments and the last visible token of this thread's rows
+        // query fragments in fp16, scaled by 2^-ex of their row, and the last visible token
+        // of this thread's rows
         uint2 qf[NR][DP / 16];
+        float undo[NR][2];  // 2^ex of rows 2 t, 2 t + 1
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const int r = row0 + n * 8 + g;
@@ -174,6 +208,31 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                 qf[n][s] = r < rows && e < d ? *reinterpret_cast<const uint2*>(qp + e)
                                              : make_uint2(0u, 0u);
             }
+            float scale = 1.f;
+            if constexpr (BF16) {
+                // bits of a bf16 magnitude order like the magnitudes
+                uint32_t mx = 0;
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    mx = max(max(mx, max(qf[n][s].x & 0x7FFFu, (qf[n][s].x >> 16) & 0x7FFFu)),
+                             max(qf[n][s].y & 0x7FFFu, (qf[n][s].y >> 16) & 0x7FFFu));
+                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                // the largest element to [2^14, 2^15); scales stay normal (an element of 2^127 or
+                // of 2^-120 is still in range), and infinities and NaN stay themselves
+                const int ex = min(max(static_cast<int>(mx >> 7) - 127 - 14, -120), 120);
+                const float down = __int_as_float((127 - ex) << 23);
+                scale = __int_as_float((127 + ex) << 23);
+                auto to_half = [&](uint32_t v) {
+                    return kv_pack_f16(cache_value<true>(static_cast<uint16_t>(v & 0xFFFFu)) * down,
+                                       cache_value<true>(static_cast<uint16_t>(v >> 16)) * down);
+                };
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    qf[n][s] = make_uint2(to_half(qf[n][s].x), to_half(qf[n][s].y));
+            }
+            undo[n][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);      // row 2 t's quad
+            undo[n][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);  // row 2 t + 1's
         }
         int at[NR][2];
 #pragma unroll
@@ -195,94 +254,111 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
         }
 
+        const int32_t* trow = a.batch.table + static_cast<int64_t>(w.b) * a.batch.width;
         auto entry_of = [&](int j0) -> int32_t {
-            return P16 && j0 < seq.len ? kv_entry(a.batch, w.b, page_index(j0)) : 0;
+            return P16 && j0 < seq.len ? __ldg(trow + page_index(j0)) : 0;
         };
-        // Where a block's rows are: offsets of token j0's row (P16), of a token's otherwise.
-        // Tokens behind the last one repeat it; the masks drop them.
+        // Element offsets of a token's row (of its scale; times d, of its codes) in the pools.
         struct Place {
             int64_t kc, vc, ks, vs;
         };
+        const uint32_t hrow = static_cast<uint32_t>(w.h) * c.ps;
         auto place = [&](int j, int32_t entry) {
-            const int64_t page = kv_page(c, entry, a.status);
-            const int64_t row = kv_row(c, w.h, j - page_index(j) * c.ps);
-            return Place{page * c.kc_page + row * d, page * c.vc_page + row * d, page * c.ks_page + row,
-                         page * c.vs_page + row};
-        };
-        auto row_of = [&](const Place& base, int j0, int r) {  // of token j0 + r
-            const int rr = min(r, seq.len - 1 - j0);
-            if constexpr (P16)
-                return Place{base.kc + rr * d, base.vc + rr * d, base.ks + rr, base.vs + rr};
-            else
-                return place(j0 + rr, kv_entry(a.batch, w.b, page_index(j0 + rr)));
-        };
-        KvBlock<DP> bk;
-        auto fetch_k = [&](int j0, const Place& base) {
-            if (j0 >= seq.len) return;  // nothing of the block is visible either
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int8_t* p = c.kc + row_of(base, j0, g + 8 * e).kc;
-#pragma unroll
-                for (int u = 0; u < U; ++u) bk.k[e][u] = kv_ldg16(p + kcol[u]);
+            const uint64_t page = static_cast<uint32_t>(kv_page(c, entry, a.status));
+            const uint32_t row = hrow + static_cast<uint32_t>(j - page_index(j) * c.ps);
+            Place p;
+            p.kc = page * c.kc_page + static_cast<uint64_t>(row) * d;
+            p.ks = page * c.ks_page + row;
+            p.vc = p.kc;
+            p.vs = p.ks;
+            if (!same) {
+                p.vc = page * c.vc_page + static_cast<uint64_t>(row) * d;
+                p.vs = page * c.vs_page + row;
             }
-        };
-        auto fetch_scales = [&](int j0, const Place& base) {
-            if (j0 >= seq.len) return;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const Place r = row_of(base, j0, g + 8 * e);
-                bk.ks[e] = __ldg(c.ks + r.ks);
-                bk.vs[e] = __ldg(c.vs + r.vs);
-            }
-        };
-        auto fetch_v = [&](int j0, const Place& base) {
-            if (j0 >= seq.len) return;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int8_t* p = c.vc + row_of(base, j0, 2 * t + (e & 1) + 8 * (e >> 1)).vc;
-                if constexpr (DP == 64) {
-                    const uint2 x = kv_ldg8(p + vcol[0]);
-                    bk.v[e][0] = x.x;
-                    bk.v[e][1] = x.y;
-                } else {
-#pragma unroll
-                    for (int u = 0; u < DP / 128; ++u) {
-                        const uint4 x = kv_ldg16(p + vcol[u]);
-                        bk.v[e][4 * u] = x.x;
-                        bk.v[e][4 * u + 1] = x.y;
-                        bk.v[e][4 * u + 2] = x.z;
-                        bk.v[e][4 * u + 3] = x.w;
-                    }
-                }
-            }
+            return p;
         };
 
-        // One block is held: its K registers take the next block's K as soon as S is
-        // computed, its V registers as soon as P V is, so each load is in flight for the
-        // other half of a step (and the 16 warps of an SM hold 64 KB between them)
-        // without a second set of registers.
-        int j0 = (tile_lo + w.tile) * kKvTile + warp * 16;
-        auto base_of = [&](int j0, int32_t entry) {
-            return P16 && j0 < seq.len ? place(j0, entry) : Place{0, 0, 0, 0};
-        };
-        Place nb = base_of(j0, entry_of(j0));
-        int32_t entry_next = nseg > 1 ? entry_of(j0 + kKvTile) : 0;
-        fetch_k(j0, nb);
-        fetch_scales(j0, nb);
-        fetch_v(j0, nb);
-        for (int s = 0; s < nseg; ++s, j0 += kKvTile) {
-            const bool more = s + 1 < nseg;
-            if (more) nb = base_of(j0 + kKvTile, entry_next);
-            if (s + 2 < nseg) entry_next = entry_of(j0 + 2 * kKvTile);
-            // nothing of this block is visible to any row: at the ends of a unit's range
-            if (j0 > at_max || (a.geom.window && j0 + 15 <= at_min - a.geom.window)) {
-                if (more) {
-                    fetch_k(j0 + kKvTile, nb);
-                    fetch_scales(j0 + kKvTile, nb);
-                    fetch_v(j0 + kKvTile, nb);
+        const int jw = (tile_lo + w.tile) * kKvTile + warp * 16;  // block 0's first token
+        uint32_t put = 0, put_sc = 0;  // stage of block i, of block i - 1
+        uint16_t sc = 0;  // a scale of the block issued last: of K in lanes 0-15, of V in 16-31
+        int32_t entry_next = entry_of(jw);
+        // starts the copy of block i of the segment into its stage and the load of its
+        // scales, and stores those of block i - 1, which have had a step to arrive
+        auto issue = [&](int i) {
+            const int j0 = jw + i * kKvTile;
+            const bool on = i < nseg && j0 < seq.len;  // else nothing of the block is visible
+            const int last = min(15, seq.len - 1 - j0), rs = min(lane & 15, last);
+            const uint32_t st = ring + put * (2 * Ring::half);
+            Place b{0, 0, 0, 0};
+            if (on) {
+                if constexpr (P16) {
+                    b = place(j0, entry_next);
+                    const int8_t* kp = c.kc + b.kc + ccol;
+                    const int8_t* vp = c.vc + b.vc + ccol;
+                    if (last == 15) {
+                        kp += crow * d;
+                        vp += crow * d;
+#pragma unroll
+                        for (int x = 0; x < Ring::copies; ++x) {
+                            const int r = crow | (x * Ring::rows);
+                            kv_cp16(st + Ring::k_at(r, cp), kp);
+                            kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp);
+                            kp += Ring::rows * d;
+                            vp += Ring::rows * d;
+                        }
+                    } else {  // tokens behind the last one repeat it; the masks drop them
+#pragma unroll 1
+                        for (int x = 0; x < Ring::copies; ++x) {
+                            const int r = crow | (x * Ring::rows), rd = min(r, last) * d;
+                            kv_cp16(st + Ring::k_at(r, cp), kp + rd);
+                            kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp + rd);
+                        }
+                    }
+                    b.ks += rs;
+                    b.vs += rs;
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < Ring::copies; ++x) {
+                        const int r = crow + x * Ring::rows, j = j0 + min(r, last);
+                        b = place(j, __ldg(trow + page_index(j)));
+                        kv_cp16(st + Ring::k_at(r, cp), c.kc + b.kc + ccol);
+                        kv_cp16(st + Ring::half + Ring::v_at(r, cp), c.vc + b.vc + ccol);
+                    }
+                    b = place(j0 + rs, __ldg(trow + page_index(j0 + rs)));
                 }
-                continue;
             }
+            kv_cp_commit();
+            if (i >= 1 && i <= nseg) {
+                const uint32_t at = ring + Ring::off_sc + put_sc * 192u + (lane & 15) * 4u;
+                const float v = cache_value<BF16>(sc);
+                if (lane < 16) {
+                    sts32(at, __float_as_uint(v * a.scale_log2));
+                } else {
+                    const KvVScale x = kv_vscale(v);
+                    sts32(at + 64u, __float_as_uint(x.lg));
+                    sts32(at + 128u, __float_as_uint(x.inv));
+                }
+            }
+            sc = 0;
+            if (on) sc = __ldg(lane < 16 ? c.ks + b.ks : c.vs + b.vs);
+            if (i + 1 < nseg) entry_next = entry_of(j0 + kKvTile);
+            put_sc = put;
+            put = put + 1 == Ring::stages ? 0 : put + 1;
+        };
+#pragma unroll 1
+        for (int i = 0; i < Ring::stages - 1; ++i) issue(i);
+        uint32_t take = 0;  // stage of block s
+#pragma unroll 1
+        for (int s = 0; s < nseg; ++s) {
+            const int j0 = jw + s * kKvTile;
+            kv_cp_wait<Ring::stages - 2>();
+            __syncwarp();  // every lane's copies of block s are there, and block s - 1 is done with
+            issue(s + Ring::stages - 1);
+            const uint32_t st = ring + take * (2 * Ring::half);
+            const uint32_t scs = ring + Ring::off_sc + take * 192u + g * 4u;
+            take = take + 1 == Ring::stages ? 0 : take + 1;
+            // nothing of this block is visible to any row: at the ends of a unit's range
+            if (j0 > at_max || (a.geom.window && j0 + 15 <= at_min - a.geom.window)) continue;
 
             // S^T = K q^T
             float x[NR][4];
@@ -290,32 +366,33 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             for (int n = 0; n < NR; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t k0[4] = {bk.k[0][u].x, bk.k[0][u].y, bk.k[0][u].z, bk.k[0][u].w};
-                const uint32_t k1[4] = {bk.k[1][u].x, bk.k[1][u].y, bk.k[1][u].z, bk.k[1][u].w};
+                const uint4 ka = lds128(st + Ring::k_at(g, u * 4 + t));
+                const uint4 kb = lds128(st + Ring::k_at(g + 8, u * 4 + t));
+                const uint32_t k0[4] = {ka.x ^ 0x80808080u, ka.y ^ 0x80808080u, ka.z ^ 0x80808080u,
+                                        ka.w ^ 0x80808080u};
+                const uint32_t k1[4] = {kb.x ^ 0x80808080u, kb.y ^ 0x80808080u, kb.z ^ 0x80808080u,
+                                        kb.w ^ 0x80808080u};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t af[4] = {q8_pair<BF16>(k0[i], 0x4140u), q8_pair<BF16>(k1[i], 0x4140u),
-                                            q8_pair<BF16>(k0[i], 0x4342u), q8_pair<BF16>(k1[i], 0x4342u)};
+                    const uint32_t af[4] = {kv_codes01(k0[i]), kv_codes01(k1[i]), kv_codes23(k0[i]),
+                                            kv_codes23(k1[i])};
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
-                        mma_16816<BF16>(x[n], af, qf[n][u * 4 + i].x, qf[n][u * 4 + i].y);
+                        mma_16816<false>(x[n], af, qf[n][u * 4 + i].x, qf[n][u * 4 + i].y);
                 }
             }
-            if (more) fetch_k(j0 + kKvTile, nb);
             // scores in log2, with the V scale; masks
-            const float sk0 = cache_value<BF16>(bk.ks[0]) * a.scale_log2;
-            const float sk1 = cache_value<BF16>(bk.ks[1]) * a.scale_log2;
-            const KvVScale v0 = kv_vscale(cache_value<BF16>(bk.vs[0]));
-            const KvVScale v1 = kv_vscale(cache_value<BF16>(bk.vs[1]));
-            if (more) fetch_scales(j0 + kKvTile, nb);
+            const float sk0 = __uint_as_float(lds32(scs)), sk1 = __uint_as_float(lds32(scs + 32u));
+            const KvVScale v0{__uint_as_float(lds32(scs + 64u)), __uint_as_float(lds32(scs + 128u))};
+            const KvVScale v1{__uint_as_float(lds32(scs + 96u)), __uint_as_float(lds32(scs + 160u))};
             const bool open = j0 + 15 <= at_min && (!a.geom.window || j0 > at_max - a.geom.window);
             bool grow = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                x[n][0] = fmaf(x[n][0], sk0, v0.lg);
-                x[n][1] = fmaf(x[n][1], sk0, v0.lg);
-                x[n][2] = fmaf(x[n][2], sk1, v1.lg);
-                x[n][3] = fmaf(x[n][3], sk1, v1.lg);
+                x[n][0] = fmaf(x[n][0], sk0 * undo[n][0], v0.lg);
+                x[n][1] = fmaf(x[n][1], sk0 * undo[n][1], v0.lg);
+                x[n][2] = fmaf(x[n][2], sk1 * undo[n][0], v1.lg);
+                x[n][3] = fmaf(x[n][3], sk1 * undo[n][1], v1.lg);
                 if (!open) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -365,28 +442,45 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             }
             // O^T += V^T P^T
 #pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                const uint32_t y0 = bk.v[0][i] ^ 0x80808080u, y1 = bk.v[1][i] ^ 0x80808080u;
-                const uint32_t y2 = bk.v[2][i] ^ 0x80808080u, y3 = bk.v[3][i] ^ 0x80808080u;
+            for (int u = 0; u < (DP == 64 ? 1 : DP / 128); ++u) {
+                uint32_t vw[4][4];  // this thread's pieces of rows 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                for (int hw = 0; hw < 2; ++hw) {
-                    const uint32_t sel = hw ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both rows
-                    const uint32_t a01 = prmt(y0, y1, sel), a23 = prmt(y2, y3, sel);
-                    const uint32_t af[4] = {sub2<false>(prmt(a01, 0x64u, 0x4140u), 0x64806480u),
-                                            sub2<false>(prmt(a01, 0x64u, 0x4342u), 0x64806480u),
-                                            sub2<false>(prmt(a23, 0x64u, 0x4140u), 0x64806480u),
-                                            sub2<false>(prmt(a23, 0x64u, 0x4342u), 0x64806480u)};
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 2 * t + (e & 1) + 8 * (e >> 1);
+                    if constexpr (DP == 64) {
+                        const uint2 y = lds64(st + Ring::half + Ring::v_at(r, g >> 1) + (g & 1) * 8);
+                        vw[e][0] = y.x;
+                        vw[e][1] = y.y;
+                    } else {
+                        const uint4 y = lds128(st + Ring::half + Ring::v_at(r, u * 8 + g));
+                        vw[e][0] = y.x;
+                        vw[e][1] = y.y;
+                        vw[e][2] = y.z;
+                        vw[e][3] = y.w;
+                    }
+                }
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        mma_16816<false>(o[2 * i + hw][n], af, pb[n][0], pb[n][1]);
+                for (int i = 0; i < (DP == 64 ? 2 : 4); ++i) {
+                    const uint32_t y0 = vw[0][i] ^ 0x80808080u, y1 = vw[1][i] ^ 0x80808080u;
+                    const uint32_t y2 = vw[2][i] ^ 0x80808080u, y3 = vw[3][i] ^ 0x80808080u;
+#pragma unroll
+                    for (int hw = 0; hw < 2; ++hw) {
+                        const uint32_t sel = hw ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both rows
+                        const uint32_t a01 = prmt(y0, y1, sel), a23 = prmt(y2, y3, sel);
+                        const uint32_t af[4] = {kv_codes01(a01), kv_codes23(a01), kv_codes01(a23),
+                                                kv_codes23(a23)};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            mma_16816<false>(o[u * 8 + 2 * i + hw][n], af, pb[n][0], pb[n][1]);
+                    }
                 }
             }
-            if (more) fetch_v(j0 + kKvTile, nb);
         }
 
         // ------------------------------------------- join of the CTA's warps
         // Element (row, pos) of O: pos = 16 i + 2 g + e for the accumulator tile i, so
         // that a warp's stores and the join's loads are free of bank conflicts.
+        __syncthreads();  // the rings are done with
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -465,26 +559,56 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             }
             __syncthreads();
             if (s_last) {
+                // The parts' weights 2^(m_p - m) first, a warp per row, then the sum: all its
+                // loads are independent.  (One running rescale over the 37 parts of a 131K-token
+                // unit took 28 us, a load's latency for each part; this takes 3.)
                 __threadfence();
-                for (int x = tid; x < R * DP / 2; x += kKvWarps * 32) {
-                    const int r = x / (DP / 2), pos = (x % (DP / 2)) * 2;
+                const int n = static_cast<int>(last_cta - first_cta) + 1;
+                // only the first of the unit's CTAs can have begun before it
+                const int first_slot = T * first_cta / P >= unit_beg ? 0 : 1;
+                auto slot_of = [&](int i) -> const float* {
+                    return a.part + (2 * (first_cta + i) + (i == 0 ? first_slot : 0)) * SLOT;
+                };
+                float* s_f = smem;            // [n][R]: m, then weights; n <= CTAs of the device
+                float* s_n = smem + n * R;    // [R] m, [R] l
+                for (int r = warp; r < R; r += kKvWarps) {
                     float mm = kKvNone, ll = 0.f;
-                    float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
-                    for (int64_t p = first_cta; p <= last_cta; ++p) {
-                        const int64_t pb = T * p / P;
-                        const float* src = a.part + (2 * p + (pb >= unit_beg ? 0 : 1)) * SLOT;
-                        const float mp = __ldcg(src + r), lp = __ldcg(src + R + r);
-                        const float2 u = __ldcg(reinterpret_cast<const float2*>(src + 2 * R + r * DP + pos));
-                        const float mn = fmaxf(mm, mp);
-                        const float f0 = kv_exp2(mm - mn), f1 = kv_exp2(mp - mn);
-                        ll = fmaf(lp, f1, ll * f0);
-                        v.x = fmaf(u.x, f1, v.x * f0);
-                        v.y = fmaf(u.y, f1, v.y * f0);
-                        mm = mn;
+                    for (int i = lane; i < n; i += 32) {
+                        const float x = __ldcg(slot_of(i) + r);
+                        s_f[i * R + r] = x;
+                        mm = fmaxf(mm, x);
                     }
-                    finish(r, pos, mm, ll, v);
+#pragma unroll
+                    for (int o2 = 16; o2 >= 1; o2 >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o2));
+                    for (int i = lane; i < n; i += 32) {
+                        const float f = kv_exp2(s_f[i * R + r] - mm);
+                        s_f[i * R + r] = f;
+                        ll = fmaf(f, __ldcg(slot_of(i) + R + r), ll);
+                    }
+#pragma unroll
+                    for (int o2 = 16; o2 >= 1; o2 >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o2);
+                    if (lane == 0) {
+                        s_n[r] = mm;
+                        s_n[R + r] = ll;
+                    }
                 }
+                __syncthreads();
+                for (int x = tid; x < R * DP / 4; x += kKvWarps * 32) {
+                    const int r = x / (DP / 4), pos = (x % (DP / 4)) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int i = 0; i < n; ++i) {
+                        const float f = s_f[i * R + r];
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(slot_of(i) + 2 * R + r * DP + pos));
+                        v.x = fmaf(f, u.x, v.x);
+                        v.y = fmaf(f, u.y, v.y);
+                        v.z = fmaf(f, u.z, v.z);
+                        v.w = fmaf(f, u.w, v.w);
+                    }
+                    finish(r, pos, s_n[r], s_n[R + r], make_float2(v.x, v.y));
+                    finish(r, pos + 2, s_n[r], s_n[R + r], make_float2(v.z, v.w));
+                }
+                __syncthreads();  // the memory goes back to the rings
             }
         }
         it += nseg;
@@ -494,7 +618,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
 
 template <int DP, int NR>
 constexpr size_t kv_attention_smem() {
-    return static_cast<size_t>(kKvWarps) * 8 * NR * (DP + 8 + 2) * 4;
+    constexpr size_t join = static_cast<size_t>(kKvWarps) * 8 * NR * (DP + 8 + 2) * 4;
+    constexpr size_t rings = static_cast<size_t>(kKvWarps) * KvRing<DP>::total;
+    return join > rings ? join : rings;
 }
 
 }  // namespace q4dev

@@ -508,24 +508,32 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                         return a.part + (2 * static_cast<int64_t>(p) + (p == first_cta ? first_slot : 0)) * SLOT;
                     };
                     float mm = kKvNone;
+#pragma unroll 4
                     for (int p = first_cta; p <= last_cta; ++p) mm = fmaxf(mm, __ldcg(slot_of(p) + r));
                     float ll = 0.f;
+#pragma unroll 4
                     for (int p = first_cta; p <= last_cta; ++p) {
                         const float* s = slot_of(p);
                         ll = fmaf(__ldcg(s + kTcaRows + r), kv_exp2(__ldcg(s + r) - mm), ll);
                     }
                     store_lse(mm, ll);
                     const float inv = inverse(ll);
-                    for (int e0 = 0; e0 < DP; e0 += 8) {
-                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int e0 = 0; e0 < DP; e0 += 32) {  // 32 loads of a part in flight
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll 1
                         for (int p = first_cta; p <= last_cta; ++p) {
                             const float* s = slot_of(p);
                             const float f = kv_exp2(__ldcg(s + r) - mm);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
+                            for (int e = 0; e < 32; ++e)
                                 v[e] = fmaf(f, __ldcg(s + 2 * kTcaRows + (e0 + e) * kTcaRows + r), v[e]);
                         }
-                        store8(e0, inv, v);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            store8(e0 + e, inv, *reinterpret_cast<float(*)[8]>(&v[e]));
                     }
                 }
             }
