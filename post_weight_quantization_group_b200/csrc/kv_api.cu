@@ -108,6 +108,7 @@ struct AttnPlan {
     bool tc;
     int nr;               // the other kernel's blocks of 8 rows of a unit
     int rows;             // rows of a unit
+    int lead;             // what beginning and ending a unit costs, in tiles
     int64_t ctas;         // at most so many
     size_t slot, bytes;   // floats of a partial slot; workspace bytes
 };
@@ -118,6 +119,7 @@ AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
     p.tc = dp <= 128 && max_new * group > kTcMinRows;
     p.nr = max_new * group <= 8 ? 1 : 2;
     p.rows = p.tc ? kTcaRows : 8 * p.nr;
+    p.lead = p.tc ? 1 : 3;
     p.ctas = static_cast<int64_t>(p.tc || dp * p.nr > 128 ? 1 : 2) * sms;
     p.slot = static_cast<size_t>(p.rows) * (dp + 2);
     p.bytes = kWsCounterBytes + 2 * static_cast<size_t>(p.ctas) * p.slot * 4;
@@ -316,7 +318,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {p.rows, kKvTile, group, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2))};
+              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), p.lead};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.out = static_cast<uint16_t*>(out);
@@ -333,7 +335,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
     const int64_t row_tiles = batch->seqs + batch->tokens * group / p.rows;
     int64_t grid = p.ctas;
-    if (row_tiles * cache->heads < grid) grid = std::min(grid, row_tiles * cache->heads * tiles);
+    if (row_tiles * cache->heads < grid) grid = std::min(grid, row_tiles * cache->heads * (tiles + p.lead));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == Q4_BF16 ? dispatch_attention<true>(a, p, grid, st)
                                    : dispatch_attention<false>(a, p, grid, st);
@@ -353,7 +355,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {kKvTile, kKvTile, q_heads / cache->heads, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2))};
+              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), 0};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.lse = lse;

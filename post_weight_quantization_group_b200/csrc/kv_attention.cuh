@@ -191,49 +191,6 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         const int rows = seq.n * a.geom.group;
         const int row0 = w.rt * R;
 
-        // query fragments in fp16, scaled by 2^-ex of their row, and the last visible token
-        // of this thread's rows
-        uint2 qf[NR][DP / 16];
-        float undo[NR][2];  // 2^ex of rows 2 t, 2 t + 1
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const int r = row0 + n * 8 + g;
-            const int tok = r / a.geom.group;
-            const int hd = r - tok * a.geom.group;
-            const uint16_t* qp = a.q + (seq.first + tok) * a.q_stride +
-                                 static_cast<int64_t>(w.h * a.geom.group + hd) * d;
-#pragma unroll
-            for (int s = 0; s < DP / 16; ++s) {
-                const int e = (s >> 2) * 64 + t * 16 + (s & 3) * 4;
-                qf[n][s] = r < rows && e < d ? *reinterpret_cast<const uint2*>(qp + e)
-                                             : make_uint2(0u, 0u);
-            }
-            float scale = 1.f;
-            if constexpr (BF16) {
-                // bits of a bf16 magnitude order like the magnitudes
-                uint32_t mx = 0;
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s)
-                    mx = max(max(mx, max(qf[n][s].x & 0x7FFFu, (qf[n][s].x >> 16) & 0x7FFFu)),
-                             max(qf[n][s].y & 0x7FFFu, (qf[n][s].y >> 16) & 0x7FFFu));
-                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                // the largest element to [2^14, 2^15); scales stay normal (an element of 2^127 or
-                // of 2^-120 is still in range), and infinities and NaN stay themselves
-                const int ex = min(max(static_cast<int>(mx >> 7) - 127 - 14, -120), 120);
-                const float down = __int_as_float((127 - ex) << 23);
-                scale = __int_as_float((127 + ex) << 23);
-                auto to_half = [&](uint32_t v) {
-                    return kv_pack_f16(cache_value<true>(static_cast<uint16_t>(v & 0xFFFFu)) * down,
-                                       cache_value<true>(static_cast<uint16_t>(v >> 16)) * down);
-                };
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s)
-                    qf[n][s] = make_uint2(to_half(qf[n][s].x), to_half(qf[n][s].y));
-            }
-            undo[n][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);      // row 2 t's quad
-            undo[n][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);  // row 2 t + 1's
-        }
         int at[NR][2];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -347,6 +304,49 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         };
 #pragma unroll 1
         for (int i = 0; i < Ring::stages - 1; ++i) issue(i);
+        // query fragments in fp16, scaled by 2^-ex of their row, and the last visible token
+        // of this thread's rows
+        uint2 qf[NR][DP / 16];
+        float undo[NR][2];  // 2^ex of rows 2 t, 2 t + 1
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int r = row0 + n * 8 + g;
+            const int tok = r / a.geom.group;
+            const int hd = r - tok * a.geom.group;
+            const uint16_t* qp = a.q + (seq.first + tok) * a.q_stride +
+                                 static_cast<int64_t>(w.h * a.geom.group + hd) * d;
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s) {
+                const int e = (s >> 2) * 64 + t * 16 + (s & 3) * 4;
+                qf[n][s] = r < rows && e < d ? *reinterpret_cast<const uint2*>(qp + e)
+                                             : make_uint2(0u, 0u);
+            }
+            float scale = 1.f;
+            if constexpr (BF16) {
+                // bits of a bf16 magnitude order like the magnitudes
+                uint32_t mx = 0;
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    mx = max(max(mx, max(qf[n][s].x & 0x7FFFu, (qf[n][s].x >> 16) & 0x7FFFu)),
+                             max(qf[n][s].y & 0x7FFFu, (qf[n][s].y >> 16) & 0x7FFFu));
+                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                // the largest element to [2^14, 2^15); scales stay normal (an element of 2^127 or
+                // of 2^-120 is still in range), and infinities and NaN stay themselves
+                const int ex = min(max(static_cast<int>(mx >> 7) - 127 - 14, -120), 120);
+                const float down = __int_as_float((127 - ex) << 23);
+                scale = __int_as_float((127 + ex) << 23);
+                auto to_half = [&](uint32_t v) {
+                    return kv_pack_f16(cache_value<true>(static_cast<uint16_t>(v & 0xFFFFu)) * down,
+                                       cache_value<true>(static_cast<uint16_t>(v >> 16)) * down);
+                };
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    qf[n][s] = make_uint2(to_half(qf[n][s].x), to_half(qf[n][s].y));
+            }
+            undo[n][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);      // row 2 t's quad
+            undo[n][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);  // row 2 t + 1's
+        }
         uint32_t take = 0;  // stage of block s
 #pragma unroll 1
         for (int s = 0; s < nseg; ++s) {
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                 __threadfence();
                 const int n = static_cast<int>(last_cta - first_cta) + 1;
                 // only the first of the unit's CTAs can have begun before it
-                const int first_slot = T * first_cta / P >= unit_beg ? 0 : 1;
+                const int first_slot = T * first_cta / P >= unit_beg - a.geom.lead ? 0 : 1;
                 auto slot_of = [&](int i) -> const float* {
                     return a.part + (2 * (first_cta + i) + (i == 0 ? first_slot : 0)) * SLOT;
                 };
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                 __syncthreads();  // the memory goes back to the rings
             }
         }
-        it += nseg;
+        it += nseg + a.geom.lead;
         if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
     }
 }

@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                     const int64_t fc = kv_owner(unit_beg, T, P);
                     g.first_cta = static_cast<int>(fc);
                     g.last_cta = static_cast<int>(kv_owner(unit_end - 1, T, P));
-                    g.first_slot = T * fc / P >= unit_beg ? 0 : 1;
+                    g.first_slot = T * fc / P >= unit_beg - a.geom.lead ? 0 : 1;
                 }
                 const int gs = sg % kTcaSegSlots;
                 if (sg >= kTcaSegSlots) ok = warp_wait(&seg_free[gs], sg / kTcaSegSlots - 1, a.status);
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[ss]);
                 }
-                it += g.tiles;
+                it += g.tiles + a.geom.lead;
                 if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
             }
         }

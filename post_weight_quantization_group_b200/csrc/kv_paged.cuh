@@ -302,11 +302,13 @@ __global__ void __launch_bounds__(256)
 // head, fewer
 // than 2^31 - 2^16 of them), R to a tile; a unit's tiles are the KT-token tiles of the cache that
 // any of its rows sees, one at least (a unit that sees nothing still writes
-// its zeros).  The units' tiles, in order, are cut into P equal ranges, one
-// per CTA, whatever the sequences' lengths.
+// its zeros).  The units lie one after another on a line, each as `lead` empty
+// places (what beginning and ending a unit costs, in tiles) and then its
+// tiles, and the line is cut into P equal ranges, one per CTA, whatever the
+// sequences' lengths.
 
 struct KvGeom {
-    int R, KT, group, heads, window;
+    int R, KT, group, heads, window, lead;
 };
 
 // Row tiles of a sequence.
@@ -329,13 +331,13 @@ __device__ __forceinline__ int64_t kv_seq_work(const KvGeom& g, const KvSeq& s) 
     int64_t sum = 0;
     for (int rt = 0; rt < rts; ++rt) {
         int lo;
-        sum += kv_tiles(g, s, rt, &lo);
+        sum += kv_tiles(g, s, rt, &lo) + g.lead;
     }
     return sum * g.heads;
 }
 
-// A place in the work: iteration `tile` (counted from the unit's first) of
-// unit (b, rt, h).
+// A place in the work: tile `tile` (counted from the unit's first) of unit
+// (b, rt, h).
 struct KvPlace {
     int b, rt, h, tile;
 };
@@ -364,11 +366,13 @@ __device__ __forceinline__ int64_t kv_block_scan(int64_t v, int64_t* sums, int64
     return v + before;
 }
 
-// Total work, this CTA's range of it and the place where the range begins.
-// Every thread of the block calls it; `sh` is shared scratch.
+// The line's length T, the number of ranges P, this CTA's range (beginning at a
+// tile: a range that holds none is empty) and the tile where it begins.  Every
+// thread of the block calls it; `sh` is shared scratch.
 struct KvLocateShared {
     int64_t sums[32];
     KvPlace place;
+    int skip;  // empty places before the first tile
 };
 template <int NT>
 __device__ __forceinline__ void kv_locate(const KvBatch& bt, const KvGeom& g, int64_t p, int64_t P,
@@ -410,23 +414,28 @@ __device__ __forceinline__ void kv_locate(const KvBatch& bt, const KvGeom& g, in
             KvPlace w{b, 0, 0, 0};
             for (;; ++w.rt) {
                 int tl;
-                const int64_t n = kv_tiles(g, s, w.rt, &tl);
+                const int64_t n = kv_tiles(g, s, w.rt, &tl) + g.lead;
                 if (x < n * g.heads) {
                     w.h = static_cast<int>(x / n);
-                    w.tile = static_cast<int>(x - w.h * n);
+                    w.tile = static_cast<int>(x - w.h * n) - g.lead;
                     break;
                 }
                 x -= n * g.heads;
             }
+            sh->skip = max(-w.tile, 0);
+            w.tile = max(w.tile, 0);
             sh->place = w;
         }
         base += t;
     }
     __syncthreads();
     *place = sh->place;
+    *beg += sh->skip;
+    if (*beg >= *end) *beg = *end = 0;
 }
 
-// The next unit (its iteration 0); the caller has checked that there is one.
+// The next unit's tile 0, g.lead places behind the last one's end; the caller
+// checks that its range goes so far.
 __device__ __forceinline__ void kv_next_unit(const KvBatch& bt, const KvGeom& g, KvPlace* w,
                                              KvSeq* s, unsigned* status) {
     w->tile = 0;
@@ -441,7 +450,7 @@ __device__ __forceinline__ void kv_next_unit(const KvBatch& bt, const KvGeom& g,
     } while (s->n == 0);
 }
 
-// CTA that owns iteration i when T iterations are cut into P ranges [T p / P, T (p + 1) / P).
+// CTA that owns place i when T places are cut into P ranges [T p / P, T (p + 1) / P).
 __device__ __forceinline__ int64_t kv_owner(int64_t i, int64_t T, int64_t P) {
     return ((i + 1) * P - 1) / T;
 }

@@ -172,8 +172,8 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         bad.c_struct()
 
 
-# The kernels' division of work (kv_paged.cuh): units in order, each with at
-# least one tile, cut into P equal ranges.
+# The kernels' division of work (kv_paged.cuh): units in order, each as `lead`
+# empty places and then its tiles, at least one, cut into P equal ranges.
 
 def _tiles(length, n, rt, R, KT, group, window):
     r0 = rt * R
@@ -186,7 +186,7 @@ def _tiles(length, n, rt, R, KT, group, window):
 
 def test_division_of_work_model():
     rng = random.Random(1)
-    for _ in range(300):
+    for _ in range(80):
         group, heads, window = rng.choice([1, 3, 8, 40]), rng.choice([1, 2, 8]), rng.choice([0, 0, 1, 100, 700])
         R, KT = rng.choice([8, 16, 128, 256]), 128
         seqs = [(rng.choice([0, 1, 127, 128, 129, rng.randint(0, 3000)]), rng.choice([0, 1, 1, rng.randint(1, 90)]))
@@ -203,17 +203,26 @@ def test_division_of_work_model():
                         assert lo * KT <= keys[0] and keys[-1] < (lo + count) * KT
                 assert (lo + count - 1) * KT < max(length, 1) + KT
                 units += [(b, rt, h, count) for h in range(heads)]
-        T = sum(u[3] for u in units)
+        lead = rng.choice([0, 1, 3])
+        T = sum(u[3] + lead for u in units)
         P = max(min(rng.choice([1, 7, 148, 296]), T), 1)
-        starts, at = [], 0
-        for u in units:
-            starts.append(at)
-            at += u[3]
-        for s, u in zip(starts, units):
-            first, last = ((s + 1) * P - 1) // T, ((s + u[3]) * P - 1) // T
-            ranges = [(T * p // P, T * (p + 1) // P) for p in range(first, last + 1)]
-            # the owners are exactly the CTAs whose ranges meet the unit
-            assert ranges[0][0] <= s < ranges[0][1] and ranges[-1][0] < s + u[3] <= ranges[-1][1]
-            if first != last:
-                # a CTA's partial slot: 0 for a range that begins in the unit, 1 for one that began before
-                assert all(lo >= s for lo, _ in ranges[1:])
+        cuts = [T * p // P for p in range(P + 1)]
+        done, at = [], 0
+        slots = {}
+        for x, (b, rt, h, count) in enumerate(units):
+            s = at + lead  # the unit's first tile
+            e = s + count
+            first, last = ((s + 1) * P - 1) // T, (e * P - 1) // T
+            holders = [p for p in range(P) if cuts[p] < e and cuts[p + 1] > s]
+            # the owners are exactly the CTAs whose ranges hold one of its tiles
+            assert holders == list(range(first, last + 1))
+            for p in holders:
+                lo, hi = max(cuts[p], s), min(cuts[p + 1], e)
+                done += [(x, t - s) for t in range(lo, hi)]
+                if len(holders) > 1:
+                    # the CTA's partial slot: 0 for the first unit it holds tiles of
+                    mine = 0 if p not in slots else 1
+                    assert mine == (0 if p > first or cuts[p] >= at else 1)
+                slots[p] = True
+            at = e
+        assert done == [(x, t) for x, u in enumerate(units) for t in range(u[3])]
