@@ -103,6 +103,9 @@ int team_size(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 // Which kernel: the tensor-core one from more than kTcMinRows rows of a
 // sequence and KV head on (head_dim up to 128), the other for decode steps.
 constexpr int64_t kTcMinRows = 16;
+// What a unit's beginning and end cost the decode kernel, in tiles (4.5 us against
+// 1.6 us a tile): a ragged batch of 32 takes 66 us with it and 87 without.
+constexpr int kKvLead = 3;
 
 struct AttnPlan {
     bool tc;
@@ -119,18 +122,25 @@ AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
     p.tc = dp <= 128 && max_new * group > kTcMinRows;
     p.nr = max_new * group <= 8 ? 1 : 2;
     p.rows = p.tc ? kTcaRows : 8 * p.nr;
-    p.lead = p.tc ? 1 : 3;
+    p.lead = p.tc ? 1 : kKvLead;
     p.ctas = static_cast<int64_t>(p.tc || dp * p.nr > 128 ? 1 : 2) * sms;
     p.slot = static_cast<size_t>(p.rows) * (dp + 2);
     p.bytes = kWsCounterBytes + 2 * static_cast<size_t>(p.ctas) * p.slot * 4;
     return p;
 }
 
-template <bool BF16, int DP, int NR>
+// At most `ctas` CTAs, and no more than there can be places in the division of work.
+int64_t attn_grid(const KvAttn& a, int64_t ctas) {
+    const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
+    const int64_t units = (a.batch.seqs + a.batch.tokens * a.geom.group / a.geom.R) * a.geom.heads;
+    return units < ctas ? std::min(ctas, units * (tiles + a.geom.lead)) : ctas;
+}
+
+template <bool BF16, int DP, int NR, bool MASS>
 q4_status run_attention(const KvAttn& a, int64_t grid, cudaStream_t st) {
-    constexpr size_t smem = kv_attention_smem<DP, NR>();
-    auto kernel = (a.pool.ps % 16) == 0 ? kv_attention_kernel<BF16, DP, NR, true>
-                                        : kv_attention_kernel<BF16, DP, NR, false>;
+    constexpr size_t smem = kv_attention_smem<DP, NR, MASS>();
+    auto kernel = (a.pool.ps % 16) == 0 ? kv_attention_kernel<BF16, DP, NR, true, MASS>
+                                        : kv_attention_kernel<BF16, DP, NR, false, MASS>;
     if (!set_kernel_attrs(kernel, static_cast<int>(smem), false)) return Q4_ERR_CUDA;
     return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kKvWarps * 32), smem, 1, true,
                      st, a);
@@ -144,19 +154,23 @@ q4_status run_attention_tc(const KvAttn& a, int64_t grid, cudaStream_t st) {
     return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kTcaThreads), smem, 1, true, st, a);
 }
 
+template <bool BF16, bool MASS>
+q4_status dispatch_rows(const KvAttn& a, int nr, int64_t grid, cudaStream_t st) {
+    switch (padded_dim(a.pool.d)) {
+        case 64: return nr == 1 ? run_attention<BF16, 64, 1, MASS>(a, grid, st)
+                                : run_attention<BF16, 64, 2, MASS>(a, grid, st);
+        case 128: return nr == 1 ? run_attention<BF16, 128, 1, MASS>(a, grid, st)
+                                 : run_attention<BF16, 128, 2, MASS>(a, grid, st);
+        default: return nr == 1 ? run_attention<BF16, 256, 1, MASS>(a, grid, st)
+                                : run_attention<BF16, 256, 2, MASS>(a, grid, st);
+    }
+}
+
 template <bool BF16>
 q4_status dispatch_attention(const KvAttn& a, const AttnPlan& p, int64_t grid, cudaStream_t st) {
-    const int dp = padded_dim(a.pool.d), nr = p.nr;
-    if (p.tc)
-        return dp == 64 ? run_attention_tc<BF16, 64>(a, grid, st) : run_attention_tc<BF16, 128>(a, grid, st);
-    switch (dp) {
-        case 64: return nr == 1 ? run_attention<BF16, 64, 1>(a, grid, st)
-                                : run_attention<BF16, 64, 2>(a, grid, st);
-        case 128: return nr == 1 ? run_attention<BF16, 128, 1>(a, grid, st)
-                                 : run_attention<BF16, 128, 2>(a, grid, st);
-        default: return nr == 1 ? run_attention<BF16, 256, 1>(a, grid, st)
-                                : run_attention<BF16, 256, 2>(a, grid, st);
-    }
+    if (!p.tc) return dispatch_rows<BF16, false>(a, p.nr, grid, st);
+    return padded_dim(a.pool.d) == 64 ? run_attention_tc<BF16, 64>(a, grid, st)
+                                      : run_attention_tc<BF16, 128>(a, grid, st);
 }
 
 template <bool BF16>
@@ -331,11 +345,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsCounterBytes);
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
-    // no more CTAs than there can be tiles
-    const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
-    const int64_t row_tiles = batch->seqs + batch->tokens * group / p.rows;
-    int64_t grid = p.ctas;
-    if (row_tiles * cache->heads < grid) grid = std::min(grid, row_tiles * cache->heads * (tiles + p.lead));
+    const int64_t grid = attn_grid(a, p.ctas);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == Q4_BF16 ? dispatch_attention<true>(a, p, grid, st)
                                    : dispatch_attention<false>(a, p, grid, st);
@@ -351,6 +361,31 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     if (batch->tokens == 0 || batch->seqs == 0) return Q4_OK;
     if (!lse || !mass) return Q4_ERR_INVALID_ARG;
     if (!aligned(lse, 4) || !aligned(mass, 4)) return Q4_ERR_ALIGNMENT;
+    const int group = q_heads / cache->heads;
+    const int sms = sm_count(current_device());
+    const int64_t max_new = std::min(batch->max_new, batch->tokens);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (max_new * group <= kTcMinRows) {  // decode steps: the rows stay and the keys go by
+        KvAttn k{};
+        k.pool = pool_of(cache);
+        k.batch = batch_of(batch, cache->page_size);
+        const int nr = max_new * group <= 8 ? 1 : 2;
+        k.geom = {8 * nr, kKvTile, group, cache->heads,
+                  static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), kKvLead};
+        if (window >= k.batch.cap) k.geom.window = 0;  // hides nothing
+        k.q = static_cast<const uint16_t*>(q);
+        k.lse = const_cast<float*>(lse);  // read
+        k.mass = mass;
+        k.mass_page = mass_stride;
+        k.q_stride = q_stride;
+        k.q_heads = q_heads;
+        k.scale_log2 = scale * 1.44269504f;
+        k.status = q4_status_word();
+        if (!k.status) return Q4_ERR_CUDA;
+        const int64_t grid = attn_grid(k, 2LL * sms);
+        return cache->dtype == Q4_BF16 ? dispatch_rows<true, true>(k, nr, grid, st)
+                                       : dispatch_rows<false, true>(k, nr, grid, st);
+    }
     KvMass a{};
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
@@ -366,12 +401,10 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     a.scale_log2 = scale * 1.44269504f;
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
-    const int sms = sm_count(current_device());
     const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
     int64_t grid = (cache->head_dim > 128 ? 1LL : 2LL) * sms;
     if (static_cast<int64_t>(batch->seqs) * cache->heads < grid)
         grid = std::min(grid, batch->seqs * cache->heads * tiles);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == Q4_BF16 ? run_mass<true>(a, grid, st) : run_mass<false>(a, grid, st);
 }
 

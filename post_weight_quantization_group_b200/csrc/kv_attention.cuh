@@ -49,7 +49,9 @@ struct KvAttn {
     KvGeom geom;
     const uint16_t* q;
     uint16_t* out;
-    float* lse;  // [tokens, q_heads] or null
+    float* lse;  // [tokens, q_heads]: written (may be null) by attention, read by mass
+    float* mass;  // [pages, heads, page_size], pages mass_page apart
+    int64_t mass_page;
     int64_t q_stride, out_stride;
     int q_heads;
     float scale_log2;  // scale * log2(e)
@@ -110,12 +112,14 @@ __device__ __forceinline__ KvVScale kv_vscale(float sv) {
 }
 
 // A warp's ring in shared memory: stages of a block's K and V codes, then of its
-// tokens' scales (sk, log2 sv, 1 / sv).
-template <int DP>
+// tokens' scales (sk, log2 sv, 1 / sv).  For the mass: K alone, with sk and the
+// tokens' places in the mass (64 bits each).
+template <int DP, bool MASS>
 struct KvRing {
-    static constexpr int stages = DP == 64 ? 5 : 3;
+    static constexpr int stages = DP == 64 ? (MASS ? 6 : 5) : (MASS ? 4 : 3);
     static constexpr uint32_t half = 16 * DP;  // bytes of a block's K, of its V
-    static constexpr uint32_t off_sc = stages * 2 * half;
+    static constexpr uint32_t stage = (MASS ? 1 : 2) * half;
+    static constexpr uint32_t off_sc = stages * stage;
     static constexpr uint32_t total = off_sc + stages * 3 * 16 * 4;
     static constexpr int lanes = DP / 16;        // lanes of a row, 16 bytes each
     static constexpr int rows = 32 / lanes;      // rows of one cp.async of the warp
@@ -143,15 +147,21 @@ __device__ __forceinline__ void kv_cp_wait() {
 }
 
 // DP: head_dim padded to 64, 128 or 256.  NR: blocks of 8 rows (R = 8 NR).
+// MASS: not attention but the weight that each token receives, given the rows'
+// log-sum-exps: mass[j, h] += sum over the rows r that see j of exp(S[r, j] - lse_r).
+// S^T has a token's rows in one quad, so its sum is a thread's and two
+// shuffles; it is added with one atomic, the token's only one where the rows
+// fit one unit and no other sequence shares the page (any order then gives the
+// same sum).
 // P16: the page size is a multiple of 16, so a block of 16 tokens is in one
 // page and its rows follow one another; else every row looks up its own page.
-template <bool BF16, int DP, int NR, bool P16>
+template <bool BF16, int DP, int NR, bool P16, bool MASS>
 __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     kv_attention_kernel(const __grid_constant__ KvAttn a) {
     constexpr int R = 8 * NR;
     constexpr int U = DP / 64, MT = DP / 16;
     constexpr int ROW = DP + 8;  // padded row of the join buffer (floats): rows 2t apart by 16 banks
-    using Ring = KvRing<DP>;
+    using Ring = KvRing<DP, MASS>;
     extern __shared__ __align__(128) float smem[];
     // the warps' rings; at the end of a segment the same memory joins their parts
     float* s_o = smem;                                // [warps][R][ROW]
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         };
         // Element offsets of a token's row (of its scale; times d, of its codes) in the pools.
         struct Place {
-            int64_t kc, vc, ks, vs;
+            int64_t kc, vc, ks, vs;  // vs: of the mass, where that is asked for
         };
         const uint32_t hrow = static_cast<uint32_t>(w.h) * c.ps;
         auto place = [&](int j, int32_t entry) {
@@ -228,7 +238,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             p.ks = page * c.ks_page + row;
             p.vc = p.kc;
             p.vs = p.ks;
-            if (!same) {
+            if constexpr (MASS) {
+                p.vs = page * a.mass_page + row;
+            } else if (!same) {
                 p.vc = page * c.vc_page + static_cast<uint64_t>(row) * d;
                 p.vs = page * c.vs_page + row;
             }
@@ -238,6 +250,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
         const int jw = (tile_lo + w.tile) * kKvTile + warp * 16;  // block 0's first token
         uint32_t put = 0, put_sc = 0;  // stage of block i, of block i - 1
         uint16_t sc = 0;  // a scale of the block issued last: of K in lanes 0-15, of V in 16-31
+        int64_t sc_mass = 0;  // or, in 16-31, a token's place in the mass
         int32_t entry_next = entry_of(jw);
         // starts the copy of block i of the segment into its stage and the load of its
         // scales, and stores those of block i - 1, which have had a step to arrive
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             const int j0 = jw + i * kKvTile;
             const bool on = i < nseg && j0 < seq.len;  // else nothing of the block is visible
             const int last = min(15, seq.len - 1 - j0), rs = min(lane & 15, last);
-            const uint32_t st = ring + put * (2 * Ring::half);
+            const uint32_t st = ring + put * Ring::stage;
             Place b{0, 0, 0, 0};
             if (on) {
                 if constexpr (P16) {
@@ -259,7 +272,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         for (int x = 0; x < Ring::copies; ++x) {
                             const int r = crow | (x * Ring::rows);
                             kv_cp16(st + Ring::k_at(r, cp), kp);
-                            kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp);
+                            if constexpr (!MASS) kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp);
                             kp += Ring::rows * d;
                             vp += Ring::rows * d;
                         }
@@ -268,7 +281,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         for (int x = 0; x < Ring::copies; ++x) {
                             const int r = crow | (x * Ring::rows), rd = min(r, last) * d;
                             kv_cp16(st + Ring::k_at(r, cp), kp + rd);
-                            kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp + rd);
+                            if constexpr (!MASS) kv_cp16(st + Ring::half + Ring::v_at(r, cp), vp + rd);
                         }
                     }
                     b.ks += rs;
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         const int r = crow + x * Ring::rows, j = j0 + min(r, last);
                         b = place(j, __ldg(trow + page_index(j)));
                         kv_cp16(st + Ring::k_at(r, cp), c.kc + b.kc + ccol);
-                        kv_cp16(st + Ring::half + Ring::v_at(r, cp), c.vc + b.vc + ccol);
+                        if constexpr (!MASS) kv_cp16(st + Ring::half + Ring::v_at(r, cp), c.vc + b.vc + ccol);
                     }
                     b = place(j0 + rs, __ldg(trow + page_index(j0 + rs)));
                 }
@@ -290,6 +303,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                 const float v = cache_value<BF16>(sc);
                 if (lane < 16) {
                     sts32(at, __float_as_uint(v * a.scale_log2));
+                } else if constexpr (MASS) {
+                    sts64(at + (lane & 15) * 4u + 64u, static_cast<uint64_t>(sc_mass));
                 } else {
                     const KvVScale x = kv_vscale(v);
                     sts32(at + 64u, __float_as_uint(x.lg));
@@ -297,7 +312,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                 }
             }
             sc = 0;
-            if (on) sc = __ldg(lane < 16 ? c.ks + b.ks : c.vs + b.vs);
+            if constexpr (MASS) {
+                sc_mass = b.vs;
+                if (on && lane < 16) sc = __ldg(c.ks + b.ks);
+            } else {
+                if (on) sc = __ldg(lane < 16 ? c.ks + b.ks : c.vs + b.vs);
+            }
             if (i + 1 < nseg) entry_next = entry_of(j0 + kKvTile);
             put_sc = put;
             put = put + 1 == Ring::stages ? 0 : put + 1;
@@ -347,6 +367,18 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             undo[n][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);      // row 2 t's quad
             undo[n][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);  // row 2 t + 1's
         }
+        float ls[NR][2];  // the rows' log-sum-exps in log2
+        if constexpr (MASS) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + n * 8 + 2 * t + e, tok = r / a.geom.group;
+                    ls[n][e] = r < rows ? 1.44269504f * __ldg(a.lse + (seq.first + tok) * a.q_heads +
+                                                              w.h * a.geom.group + r - tok * a.geom.group)
+                                        : 0.f;
+                }
+        }
         uint32_t take = 0;  // stage of block s
 #pragma unroll 1
         for (int s = 0; s < nseg; ++s) {
@@ -354,7 +386,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             kv_cp_wait<Ring::stages - 2>();
             __syncwarp();  // every lane's copies of block s are there, and block s - 1 is done with
             issue(s + Ring::stages - 1);
-            const uint32_t st = ring + take * (2 * Ring::half);
+            const uint32_t st = ring + take * Ring::stage;
             const uint32_t scs = ring + Ring::off_sc + take * 192u + g * 4u;
             take = take + 1 == Ring::stages ? 0 : take + 1;
             // nothing of this block is visible to any row: at the ends of a unit's range
@@ -383,9 +415,33 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             }
             // scores in log2, with the V scale; masks
             const float sk0 = __uint_as_float(lds32(scs)), sk1 = __uint_as_float(lds32(scs + 32u));
+            const bool open = j0 + 15 <= at_min && (!a.geom.window || j0 > at_max - a.geom.window);
+            if constexpr (MASS) {
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + g + 8 * (e >> 1), top = at[n][e & 1];
+                        const float y = fmaf(x[n][e], (e >> 1 ? sk1 : sk0) * undo[n][e & 1], -ls[n][e & 1]);
+                        // a row of the tile that is none sees nothing (its top is -1)
+                        const bool see = (open && top >= 0) ||
+                                         (j <= top && (!a.geom.window || j > top - a.geom.window));
+                        sum[e >> 1] += see ? kv_exp2(y) : 0.f;
+                    }
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    sum[f] += __shfl_xor_sync(0xFFFFFFFFu, sum[f], 1);
+                    sum[f] += __shfl_xor_sync(0xFFFFFFFFu, sum[f], 2);
+                    if (t == 0 && j0 + g + 8 * f < seq.len) {
+                        const uint2 o = lds64(scs + g * 4u + 64u + 64u * f);
+                        atomicAdd(a.mass + ((static_cast<int64_t>(o.y) << 32) | o.x), sum[f]);
+                    }
+                }
+                continue;
+            }
             const KvVScale v0{__uint_as_float(lds32(scs + 64u)), __uint_as_float(lds32(scs + 128u))};
             const KvVScale v1{__uint_as_float(lds32(scs + 96u)), __uint_as_float(lds32(scs + 160u))};
-            const bool open = j0 + 15 <= at_min && (!a.geom.window || j0 > at_max - a.geom.window);
             bool grow = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -477,6 +533,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             }
         }
 
+        if constexpr (MASS) {
+            __syncwarp();  // the ring is done with
+            it += nseg + a.geom.lead;
+            if (it < end) kv_next_unit(a.batch, a.geom, &w, &seq, a.status);
+            continue;
+        }
         // ------------------------------------------- join of the CTA's warps
         // Element (row, pos) of O: pos = 16 i + 2 g + e for the accumulator tile i, so
         // that a warp's stores and the join's loads are free of bank conflicts.
@@ -616,11 +678,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     }
 }
 
-template <int DP, int NR>
+template <int DP, int NR, bool MASS>
 constexpr size_t kv_attention_smem() {
     constexpr size_t join = static_cast<size_t>(kKvWarps) * 8 * NR * (DP + 8 + 2) * 4;
-    constexpr size_t rings = static_cast<size_t>(kKvWarps) * KvRing<DP>::total;
-    return join > rings ? join : rings;
+    constexpr size_t rings = static_cast<size_t>(kKvWarps) * KvRing<DP, MASS>::total;
+    return MASS || rings > join ? rings : join;
 }
 
 }  // namespace q4dev
