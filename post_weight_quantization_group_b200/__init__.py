@@ -17,6 +17,7 @@ the KV-cache calls ``kv_quantize_int8``, ``kv_dequant_int8``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -628,18 +629,15 @@ class KVPagedInt8:
         shape = kc.shape
         if kc.dtype != torch.int8 or vc.dtype != torch.int8 or len(shape) != 4 or vc.shape != shape:
             raise ValueError("k_codes and v_codes must be int8 [pages, heads, page_size, head_dim]")
-        if ks.dtype not in _DT or vs.dtype != ks.dtype or ks.shape != shape[:3] or vs.shape != shape[:3]:
+        dt = ks.dtype
+        if dt not in _DT or vs.dtype != dt or ks.shape != shape[:3] or vs.shape != shape[:3]:
             raise ValueError("k_scales and v_scales must be [pages, heads, page_size] of one 16-bit type")
         pages, heads, ps, d = shape
-        strides = []
-        for x, inner in ((kc, (ps * d, d, 1)), (ks, (ps, 1)), (vc, (ps * d, d, 1)), (vs, (ps, 1))):
-            st = x.stride()
-            if not _dense(x.shape[1:], st[1:], inner):
-                raise ValueError("a page's codes and scales must be dense")
-            strides.append(st[0] if pages > 1 else heads * inner[0])
         _same_device(kc, ks, vc, vs)
-        return _CKVPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *strides, pages,
-                         heads, ps, d, _DT[ks.dtype])
+        return _CKVPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                         _page_stride(kc, heads * ps * d), _page_stride(ks, heads * ps),
+                         _page_stride(vc, heads * ps * d), _page_stride(vs, heads * ps), pages,
+                         heads, ps, d, _DT[dt])
 
 
 def kv_paged_int8(pages: int, heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16,
@@ -652,9 +650,14 @@ def kv_paged_int8(pages: int, heads: int, page_size: int, head_dim: int, dtype=t
                        torch.zeros(shape[:3], dtype=dtype, device=device))
 
 
-def _dense(shape, strides, want) -> bool:
-    """Strides as wanted, but for dimensions of one element."""
-    return all(n <= 1 or s == w for n, s, w in zip(shape, strides, want))
+def _page_stride(x: torch.Tensor, dense: int) -> int:
+    """Elements from a page (the first dimension) to the next; ``dense`` is a
+    page's own size, inside which nothing may lie apart."""
+    if x.is_contiguous():
+        return dense
+    if not x[0].is_contiguous():
+        raise ValueError("what lies inside a page, or inside a token, must be dense")
+    return x.stride(0) if x.shape[0] > 1 else dense
 
 
 def _same_device(first: torch.Tensor, *rest):
@@ -674,14 +677,14 @@ class _Call:
 
     def __init__(self, device: torch.device, stream):
         self.device = device
-        cur = torch.cuda.current_stream(device)
-        self.handle = cur.cuda_stream if stream is None else _stream(stream)
+        current = torch._C._cuda_getCurrentRawStream(device.index)
+        self.handle = current if stream is None else _stream(stream)
         self._ctx = None
-        if self.handle != cur.cuda_stream:
+        if self.handle != current:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(self.handle, device=device)
             self._ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
+        elif device.index != torch._C._cuda_getDevice():
             self._ctx = torch.cuda.device(device)
 
     def __enter__(self):
@@ -713,16 +716,19 @@ _WS_COUNTER_BYTES = 256 * 1024  # the counters at the head of a workspace
 _stream_workspaces: dict = {}
 
 
+@functools.lru_cache(maxsize=256)
+def _kv_workspace_bytes(device: int, *shape: int) -> int:
+    """kv_attention_workspace_bytes, which depends on the device's SM count and
+    these numbers alone (called with that device current)."""
+    return int(load_library().kv_attention_workspace_bytes(*shape))
+
+
 def _head_rows(t: torch.Tensor, what: str, heads: int | None, d: int, dtype, tokens: int | None = None):
     """Checks [tokens, heads, head_dim] with dense heads; returns the row stride."""
     if t.dim() != 3 or t.dtype != dtype or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
             or (tokens is not None and t.shape[0] != tokens):
         raise ValueError(f"{what} must be [tokens, heads, head_dim] in the cache type")
-    n, h, _ = t.shape
-    st = t.stride()
-    if not _dense((h, d), st[1:], (d, 1)):
-        raise ValueError(f"{what}: the heads of a token must be dense")
-    return st[0] if n > 1 else h * d
+    return _page_stride(t, t.shape[1] * d)
 
 
 def _int32(t: torch.Tensor | None, what: str, shape):
@@ -841,7 +847,7 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
         os_ = _head_rows(out, "out", hq, d, dt, tokens)
         if workspace is None:
             workspace = call.workspace(
-                int(lib.kv_attention_workspace_bytes(d, hq, cs.heads, max(1, min(max_new, tokens)))))
+                _kv_workspace_bytes(q.device.index, d, hq, cs.heads, max(1, min(max_new, tokens))))
         st = lib.kv_attention_int8_paged(
             ctypes.byref(cs), q.data_ptr(), qs, hq, ctypes.byref(batch),
             d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lse.data_ptr(),
@@ -877,10 +883,9 @@ def kv_attention_mass_int8_paged(cache: KVPagedInt8, q: torch.Tensor, lse: torch
 
 def _mass_stride(cache: KVPagedInt8, mass: torch.Tensor) -> int:
     pages, heads, ps = cache.k_scales.shape
-    if mass.dtype != torch.float32 or tuple(mass.shape) != (pages, heads, ps) \
-            or not _dense((heads, ps), mass.stride()[1:], (ps, 1)):
-        raise ValueError("mass must be fp32 [pages, heads, page_size], a page dense")
-    return mass.stride(0) if pages > 1 else heads * ps
+    if mass.dtype != torch.float32 or mass.shape != (pages, heads, ps):
+        raise ValueError("mass must be fp32 [pages, heads, page_size]")
+    return _page_stride(mass, heads * ps)
 
 
 def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: torch.Tensor,

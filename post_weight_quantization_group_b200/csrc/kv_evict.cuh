@@ -42,132 +42,232 @@ __device__ __forceinline__ uint32_t kv_mass_key(float m) {
 }
 
 constexpr int kEvThreads = 1024;
-constexpr int kEvHeld = 32;  // keys a thread keeps in registers: 32,768 tokens need no second read
+constexpr int kEvHeld = 4;  // times four keys that a thread keeps in registers: 16,384 tokens of a CTA
 
-// The kept tokens of one (sequence, KV head): the mass of rank K = budget -
-// sinks - recent among the others is found digit by digit from the top (four
-// histograms of 8 bits), then one pass in order writes the tokens above it and
-// the first of those equal to it.
-__global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __grid_constant__ KvEvict a) {
-    __shared__ uint32_t hist[256];
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The kept tokens of one (sequence, KV head), by a cluster of C CTAs that take
+// C consecutive parts of the sequence: the mass of rank K = budget - sinks -
+// recent among the tokens that compete is found digit by digit from the top
+// (four histograms of 8 bits, added up through distributed shared memory),
+// then one pass in order writes the tokens above it and the first of those
+// equal to it, each CTA behind what the ones before it wrote.  Bound by
+// latency: 8 heads of 32,768 tokens took 100 us in 8 CTAs.  A thread takes four
+// consecutive tokens at a time (one 16-byte load where vec allows).
+__global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __grid_constant__ KvEvict a, int C,
+                                                                    int vec) {
+    __shared__ uint32_t hist[4][256];
     __shared__ uint32_t s_digit, s_rank;
-    __shared__ uint32_t s_warp[2][32];
+    __shared__ uint32_t s_warp[32];
+    __shared__ uint32_t s_count[2];  // this CTA's tokens above the border, and at it
     grid_launch_dependents();
     grid_dependency_wait();
     const KvPool& c = a.pool;
-    const int b = blockIdx.x / c.heads, h = blockIdx.x - b * c.heads;
+    const int unit = blockIdx.x / C, part = blockIdx.x - unit * C;
+    const int b = unit / c.heads, h = unit - b * c.heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = kv_evict_len(a, b);
-    if (h == 0 && tid == 0) a.len[b] = len;
+    if (h == 0 && part == 0 && tid == 0) a.len[b] = len;
     if (len <= a.budget) return;  // all are kept: the move knows
-    int32_t* src = a.src + (static_cast<int64_t>(b) * c.heads + h) * a.budget;
+    int32_t* src = a.src + static_cast<int64_t>(unit) * a.budget;
+    reinterpret_cast<uint32_t*>(hist)[tid] = 0;
 
-    // the tokens that compete: [lo, hi), K of them stay
+    // the tokens that compete: [lo, hi), K of them stay; this CTA's: [j_beg, j_end)
     const int lo = a.sinks, hi = len - a.recent;
     const int K = a.budget - a.sinks - a.recent;
-    const int n = hi - lo;
-    auto key_at = [&](int j) -> uint32_t {
-        const int64_t page = kv_page(c, kv_entry(a.batch, b, j / c.ps), a.status);
-        return kv_mass_key(__ldg(a.mass + page * a.mass_page + kv_row(c, h, j % c.ps)));
-    };
-    uint32_t held[kEvHeld];
+    const int chunk = ((len + C - 1) / C + 3) & ~3;
+    const int j_beg = part * chunk, j_end = min(j_beg + chunk, len);
+    const int steps = j_end > j_beg ? (j_end - j_beg + 4 * kEvThreads - 1) / (4 * kEvThreads) : 0;
+    const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;
+    const int32_t* trow = a.batch.table + static_cast<int64_t>(b) * a.batch.width;
+    const float* mass = a.mass + static_cast<int64_t>(h) * c.ps;
+    auto in = [&](int j) { return j >= lo && j < hi && j < j_end; };
+    // keys of tokens j .. j + 3 (a multiple of four); 0 where there is none
+    auto keys_at = [&](int j, uint32_t (&k)[4]) {
+        k[0] = k[1] = k[2] = k[3] = 0u;
+        if (j >= j_end) return;
+        if (vec) {
+            const int e = shift >= 0 ? j >> shift : j / c.ps;
+            const int64_t page = kv_page(c, __ldg(trow + e), a.status);
+            const float4 m = __ldg(reinterpret_cast<const float4*>(mass + page * a.mass_page + (j - e * c.ps)));
+            k[0] = kv_mass_key(m.x);
+            k[1] = kv_mass_key(m.y);
+            k[2] = kv_mass_key(m.z);
+            k[3] = kv_mass_key(m.w);
+        } else {
 #pragma unroll
-    for (int i = 0; i < kEvHeld; ++i) {
-        const int x = i * kEvThreads + tid;
-        held[i] = x < n ? key_at(lo + x) : 0u;
-    }
+            for (int i = 0; i < 4; ++i) {
+                if (j + i >= j_end) break;
+                const int e = shift >= 0 ? (j + i) >> shift : (j + i) / c.ps;
+                const int64_t page = kv_page(c, __ldg(trow + e), a.status);
+                k[i] = kv_mass_key(__ldg(mass + page * a.mass_page + (j + i - e * c.ps)));
+            }
+        }
+    };
+    auto first_of = [&](int step) { return j_beg + (step * kEvThreads + tid) * 4; };
+    uint32_t held[kEvHeld][4];
+#pragma unroll
+    for (int s = 0; s < kEvHeld; ++s) keys_at(first_of(s), held[s]);
+    __syncthreads();  // the histograms are zero
 
     // the K-th largest key: `prefix`, and `rank` of the keys equal to it stay
     uint32_t prefix = 0, mask = 0, rank = static_cast<uint32_t>(K);
-    if (K > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            auto add = [&](uint32_t k, bool in) {
-                // neighbours often share a digit (tokens nobody looked at): one add for equal ones
-                const bool use = in && (k & mask) == prefix;
-                const uint32_t dg = use ? (k >> shift) & 255u : 256u;
-                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, dg);
-                if (use && lane == __ffs(peers) - 1) atomicAdd(&hist[dg], __popc(peers));
-            };
+    for (int pass = 0; pass < 4; ++pass) {
+        const int sh = 24 - 8 * pass;
+        auto add = [&](const uint32_t (&k)[4], int j) {
 #pragma unroll
-            for (int i = 0; i < kEvHeld; ++i)
-                if (i * kEvThreads < n) add(held[i], i * kEvThreads + tid < n);
-            for (int x0 = kEvHeld * kEvThreads; x0 < n; x0 += kEvThreads) {
-                const bool in = x0 + tid < n;
-                add(in ? key_at(lo + x0 + tid) : 0u, in);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // counts of the digits from the top: lane holds digits 255 - 8 lane - i
-                uint32_t cnt[8], sum = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum += cnt[i] = hist[255 - 8 * lane - i];
-                uint32_t incl = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                    if (lane >= o) incl += u;
-                }
-                uint32_t above = incl - sum;
-                if (above < rank && rank <= incl) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (above < rank && rank <= above + cnt[i]) {
-                            s_digit = 255 - 8 * lane - i;
-                            s_rank = rank - above;
-                        }
-                        above += cnt[i];
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const bool use = in(j + i) && (k[i] & mask) == prefix;
+                // many tokens that nobody looked at share a key: one add for a warp of them
+                const uint32_t dg = use ? (k[i] >> sh) & 255u : 256u;
+                int same;
+                __match_all_sync(0xFFFFFFFFu, dg, &same);
+                if (same) {
+                    if (use && lane == 0) atomicAdd(&hist[pass][dg], 32u);
+                } else if (use) {
+                    atomicAdd(&hist[pass][dg], 1u);
                 }
             }
-            __syncthreads();
-            prefix |= s_digit << shift;
-            mask |= 255u << shift;
-            rank = s_rank;
+        };
+#pragma unroll
+        for (int s = 0; s < kEvHeld; ++s)
+            if (s < steps) add(held[s], first_of(s));
+        for (int s = kEvHeld; s < steps; ++s) {
+            uint32_t k[4];
+            keys_at(first_of(s), k);
+            add(k, first_of(s));
+        }
+        if (C > 1) {
+            cluster_sync_all();
+        } else {
             __syncthreads();
         }
+        if (warp == 0) {
+            // counts of the digits from the top: lane holds digits 255 - 8 lane - i
+            uint32_t cnt[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cnt[i] = 0;
+            for (int q = 0; q < C; ++q) {
+                const uint32_t at = C > 1 ? mapa_shared(smem_u32(&hist[pass][0]), q) : smem_u32(&hist[pass][0]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) cnt[i] += ld_shared_cluster_u32(at + (255 - 8 * lane - i) * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += cnt[i];
+            uint32_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            uint32_t above = incl - sum;
+            if (K > 0 && above < rank && rank <= incl) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (above < rank && rank <= above + cnt[i]) {
+                        s_digit = 255 - 8 * lane - i;
+                        s_rank = rank - above;
+                    }
+                    above += cnt[i];
+                }
+            }
+        }
+        __syncthreads();
+        if (K > 0) {
+            prefix |= s_digit << sh;
+            mask |= 255u << sh;
+            rank = s_rank;
+        }
+        __syncthreads();  // the next pass writes s_digit
+    }
+
+    // this CTA's tokens above the border and at it, and what stands before them
+    auto counts_of = [&](const uint32_t (&k)[4], int j) {  // two counts of at most 4
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (in(j + i)) n += k[i] > prefix ? 1u : k[i] == prefix ? 1u << 16 : 0u;
+        return n;
+    };
+    uint32_t done = 0, ties = 0;  // tokens above the border, and at it, in earlier parts and steps
+    if (C > 1) {
+        uint32_t n = 0, gt = 0, eq = 0;
+#pragma unroll
+        for (int s = 0; s < kEvHeld; ++s)
+            if (s < steps) n += counts_of(held[s], first_of(s));
+        gt = n & 0xFFFFu;
+        eq = n >> 16;
+        for (int s = kEvHeld; s < steps; ++s) {
+            uint32_t k[4];
+            keys_at(first_of(s), k);
+            n = counts_of(k, first_of(s));
+            gt += n & 0xFFFFu;
+            eq += n >> 16;
+        }
+        if (tid < 2) s_count[tid] = 0;
+        __syncthreads();
+        gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+        eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+        if (lane == 0) {
+            atomicAdd(&s_count[0], gt);
+            atomicAdd(&s_count[1], eq);
+        }
+        cluster_sync_all();
+        for (int q = 0; q < part; ++q) {
+            const uint32_t at = mapa_shared(smem_u32(s_count), q);
+            done += ld_shared_cluster_u32(at);
+            ties += ld_shared_cluster_u32(at + 4);
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its shared memory
     }
 
     // in order: sinks, those above the border and the first `rank` at it, recent
-    for (int j = tid; j < a.sinks; j += kEvThreads) src[j] = j;
-    for (int j = tid; j < a.recent; j += kEvThreads) src[a.budget - a.recent + j] = hi + j;
+    if (part == 0) {
+        for (int j = tid; j < a.sinks; j += kEvThreads) src[j] = j;
+        for (int j = tid; j < a.recent; j += kEvThreads) src[a.budget - a.recent + j] = hi + j;
+    }
     if (K == 0) return;
-    uint32_t done = 0, ties = 0;  // written, and border keys seen, in earlier steps
-    auto emit = [&](uint32_t k, int x, bool in) {
-        const bool gt = in && k > prefix, eq = in && k == prefix;
-        const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
-        if (lane == 0) {
-            s_warp[0][warp] = __popc(bg);
-            s_warp[1][warp] = __popc(be);
-        }
-        __syncthreads();
-        uint32_t g0 = 0, e0 = 0, gall = 0, eall = 0;
+    auto emit = [&](const uint32_t (&k)[4], int j) {
+        const uint32_t n = counts_of(k, j);
+        uint32_t incl = n;  // two 16-bit sums: a step has 4096 tokens
 #pragma unroll
-        for (int w = 0; w < 32; ++w) {
-            const uint32_t u = s_warp[0][w], v = s_warp[1][w];
-            if (w < warp) {
-                g0 += u;
-                e0 += v;
-            }
-            gall += u;
-            eall += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += u;
         }
-        const uint32_t below = (1u << lane) - 1u;
-        g0 += __popc(bg & below);
-        const uint32_t er = ties + e0 + __popc(be & below);  // border keys before this one
-        if (gt || (eq && er < rank))
-            src[a.sinks + done + g0 + (min(er, rank) - min(ties, rank))] = lo + x;
-        done += gall + min(ties + eall, rank) - min(ties, rank);
-        ties += eall;
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        const uint32_t w = s_warp[lane];
+        uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
+        const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, w);
+        before += incl - n;
+        uint32_t g = done + (before & 0xFFFFu), e = ties + (before >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!in(j + i)) continue;
+            if (k[i] > prefix) {
+                src[a.sinks + g + min(e, rank)] = j + i;
+                ++g;
+            } else if (k[i] == prefix) {
+                if (e < rank) src[a.sinks + g + e] = j + i;
+                ++e;
+            }
+        }
+        done += all & 0xFFFFu;
+        ties += all >> 16;
         __syncthreads();
     };
 #pragma unroll
-    for (int i = 0; i < kEvHeld; ++i)
-        if (i * kEvThreads < n) emit(held[i], i * kEvThreads + tid, i * kEvThreads + tid < n);
-    for (int x0 = kEvHeld * kEvThreads; x0 < n; x0 += kEvThreads) {
-        const bool in = x0 + tid < n;
-        emit(in ? key_at(lo + x0 + tid) : 0u, x0 + tid, in);
+    for (int s = 0; s < kEvHeld; ++s)
+        if (s < steps) emit(held[s], first_of(s));
+    for (int s = kEvHeld; s < steps; ++s) {
+        uint32_t k[4];
+        keys_at(first_of(s), k);
+        emit(k, first_of(s));
     }
 }
 
