@@ -627,7 +627,7 @@ class KVPagedInt8:
     def c_struct(self) -> _CKVPaged:
         kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
         shape = kc.shape
-        if kc.dtype != torch.int8 or vc.dtype != torch.int8 or len(shape) != 4 or vc.shape != shape:
+        if kc.dtype is not torch.int8 or vc.dtype is not torch.int8 or len(shape) != 4 or vc.shape != shape:
             raise ValueError("k_codes and v_codes must be int8 [pages, heads, page_size, head_dim]")
         dt = ks.dtype
         if dt not in _DT or vs.dtype != dt or ks.shape != shape[:3] or vs.shape != shape[:3]:
@@ -732,7 +732,7 @@ def _head_rows(t: torch.Tensor, what: str, heads: int | None, d: int, dtype, tok
 
 
 def _int32(t: torch.Tensor | None, what: str, shape):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
 
 
@@ -766,7 +766,7 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
     ks = _head_rows(k, "k", cs.heads, d, dt)
     vs = _head_rows(v, "v", cs.heads, d, dt, tokens)
     qs = _head_rows(q, "q", None, d, dt, tokens) if q is not None else 0
-    if slots.dtype != torch.int64 or tuple(slots.shape) != (tokens,) or not slots.is_contiguous():
+    if slots.dtype != torch.int64 or slots.shape != (tokens,) or not slots.is_contiguous():
         raise ValueError("slots must be contiguous int64 [tokens]")
     rot = 0
     if inv_freq is not None:
@@ -777,12 +777,12 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
         rot = 2 * inv_freq.shape[0]
         _int32(positions, "positions", (tokens,))
     for w in (q_norm, k_norm):
-        if w is not None and (w.dtype != dt or tuple(w.shape) != (d,) or not w.is_contiguous()):
+        if w is not None and (w.dtype != dt or w.shape != (d,) or not w.is_contiguous()):
             raise ValueError("norm weights must be [head_dim] in the cache type")
     _same_device(cache.k_codes, q, k, v, slots, positions, inv_freq, q_norm, k_norm, q_out)
     with _Call(k.device, stream) as call:
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+            q_out = q.new_empty(q.shape)
         os_ = _head_rows(q_out, "q_out", q.shape[1], d, dt, tokens) if q is not None else 0
         st = lib.kv_append_int8_paged(
             ctypes.byref(cs), q.data_ptr() if q is not None else None, qs,
@@ -808,11 +808,11 @@ def kv_gather_int8_paged(cache: KVPagedInt8, slots: torch.Tensor, k_out: torch.T
     _same_device(cache.k_codes, slots, k_out, v_out)
     with _Call(slots.device, stream) as call:
         if k_out is None:
-            k_out = torch.empty(shape, dtype=cache.dtype, device=slots.device)
+            k_out = cache.k_scales.new_empty(shape)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=cache.dtype, device=slots.device)
+            v_out = cache.k_scales.new_empty(shape)
         for x in (k_out, v_out):
-            if x.dtype != cache.dtype or tuple(x.shape) != shape or not x.is_contiguous():
+            if x.dtype != cache.dtype or x.shape != shape or not x.is_contiguous():
                 raise ValueError("k_out and v_out must be contiguous [tokens, heads, head_dim] in the cache type")
         st = lib.kv_gather_int8_paged(ctypes.byref(cs), slots.data_ptr(), shape[0], k_out.data_ptr(),
                                       v_out.data_ptr(), call.handle)
@@ -839,10 +839,10 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     _same_device(cache.k_codes, q, block_table, seq_lens, cu_new, out, lse, workspace)
     with _Call(q.device, stream) as call:
         if out is None:
-            out = torch.empty(q.shape, dtype=dt, device=q.device)
+            out = q.new_empty(q.shape)
         if lse is None:
-            lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, hq) or not lse.is_contiguous():
+            lse = q.new_empty((tokens, hq), dtype=torch.float32)
+        elif lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous fp32 [tokens, q_heads]")
         os_ = _head_rows(out, "out", hq, d, dt, tokens)
         if workspace is None:
@@ -868,7 +868,7 @@ def kv_attention_mass_int8_paged(cache: KVPagedInt8, q: torch.Tensor, lse: torch
     cs = cache.c_struct()
     tokens, hq = q.shape[0], q.shape[1]
     qs = _head_rows(q, "q", None, cs.head_dim, cache.dtype)
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, hq) or not lse.is_contiguous():
+    if lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [tokens, q_heads]")
     ms = _mass_stride(cache, mass)
     batch = _kv_batch(block_table, seq_lens, cu_new, tokens, max_new)
@@ -909,10 +909,10 @@ def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: tor
     _same_device(cache.k_codes, mass, block_table, seq_lens, dst_table, new_lens, workspace)
     with _Call(seq_lens.device, stream) as call:
         if new_lens is None:
-            new_lens = torch.empty(seqs, dtype=torch.int32, device=seq_lens.device)
+            new_lens = seq_lens.new_empty(seqs)
         if workspace is None:
             need = int(lib.kv_evict_workspace_bytes(seqs, cs.heads, budget))
-            workspace = torch.empty(need, dtype=torch.uint8, device=seq_lens.device)
+            workspace = seq_lens.new_empty(need, dtype=torch.uint8)
         st = lib.kv_evict_int8_paged(
             ctypes.byref(cs), mass.data_ptr(), ms, ctypes.byref(batch), budget, recent, sinks,
             dst_table.data_ptr() if dst_table is not None else None,
