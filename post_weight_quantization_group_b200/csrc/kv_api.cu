@@ -16,6 +16,7 @@
 #include "kv_attention.cuh"
 #include "kv_attention_tc.cuh"
 #include "kv_mass.cuh"
+#include "kv_mass_tc.cuh"
 #include "kv_evict.cuh"
 
 namespace {
@@ -173,14 +174,19 @@ q4_status dispatch_attention(const KvAttn& a, const AttnPlan& p, int64_t grid, c
                                       : run_attention_tc<BF16, 128>(a, grid, st);
 }
 
+template <bool BF16, int DP>
+q4_status run_mass_tc(const KvMassTc& a, int64_t grid, cudaStream_t st) {
+    constexpr size_t smem = TcmGeom<DP>::total;
+    auto kernel = kv_mass_tc_kernel<BF16, DP>;
+    if (!set_kernel_attrs(kernel, static_cast<int>(smem), false)) return Q4_ERR_CUDA;
+    return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kTcaThreads), smem, 1, true, st, a);
+}
+
+// Chunks with head_dim above 128.
 template <bool BF16>
 q4_status run_mass(const KvMass& a, int64_t grid, cudaStream_t st) {
-    const dim3 gd(static_cast<unsigned>(grid)), bd(kKvWarps * 32);
-    switch (padded_dim(a.pool.d)) {
-        case 64: return launch_ex(kv_mass_kernel<BF16, 64>, gd, bd, 0, 1, true, st, a);
-        case 128: return launch_ex(kv_mass_kernel<BF16, 128>, gd, bd, 0, 1, true, st, a);
-        default: return launch_ex(kv_mass_kernel<BF16, 256>, gd, bd, 0, 1, true, st, a);
-    }
+    return launch_ex(kv_mass_kernel<BF16, 256>, dim3(static_cast<unsigned>(grid)), dim3(kKvWarps * 32), 0,
+                     1, true, st, a);
 }
 
 template <bool BF16>
@@ -386,6 +392,28 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
         return cache->dtype == Q4_BF16 ? dispatch_rows<true, true>(k, nr, grid, st)
                                        : dispatch_rows<false, true>(k, nr, grid, st);
     }
+    if (cache->head_dim <= 128) {
+        KvMassTc k{};
+        k.pool = pool_of(cache);
+        k.batch = batch_of(batch, cache->page_size);
+        k.group = group;
+        k.window = window >= k.batch.cap ? 0 : static_cast<int>(window);
+        k.q_heads = q_heads;
+        k.q = static_cast<const uint16_t*>(q);
+        k.lse = lse;
+        k.mass = mass;
+        k.q_stride = q_stride;
+        k.mass_page = mass_stride;
+        k.scale_log2 = scale * 1.44269504f;
+        k.status = q4_status_word();
+        if (!k.status) return Q4_ERR_CUDA;
+        const int64_t keys = std::max<int64_t>((k.batch.cap + 127) / 128, 1);
+        const int64_t units = static_cast<int64_t>(batch->seqs) * cache->heads;
+        const int64_t grid = units < sms ? std::min<int64_t>(sms, units * keys) : sms;
+        if (cache->dtype == Q4_BF16)
+            return cache->head_dim <= 64 ? run_mass_tc<true, 64>(k, grid, st) : run_mass_tc<true, 128>(k, grid, st);
+        return cache->head_dim <= 64 ? run_mass_tc<false, 64>(k, grid, st) : run_mass_tc<false, 128>(k, grid, st);
+    }
     KvMass a{};
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
@@ -402,7 +430,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
     const int64_t tiles = std::max<int64_t>((a.batch.cap + kKvTile - 1) / kKvTile, 1);
-    int64_t grid = (cache->head_dim > 128 ? 1LL : 2LL) * sms;
+    int64_t grid = sms;
     if (static_cast<int64_t>(batch->seqs) * cache->heads < grid)
         grid = std::min(grid, batch->seqs * cache->heads * tiles);
     return cache->dtype == Q4_BF16 ? run_mass<true>(a, grid, st) : run_mass<false>(a, grid, st);
