@@ -176,29 +176,35 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
                     uint32_t v[32];
                     tmem_ld16(td + 32 * q, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
                     tmem_ld16(td + 32 * q + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                    uint4 l4[8];  // -lse of the chunk's rows
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) l4[e] = lds128(ls + 128u * q + 16u * e);
                     tmem_wait_ld();
+                    float x[32];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const uint4 l4 = lds128(ls + 128u * q + 16u * e);  // -lse of four rows
-                        const uint32_t lw[4] = {l4.x, l4.y, l4.z, l4.w};
+                        const uint32_t lw[4] = {l4[e].x, l4[e].y, l4[e].z, l4[e].w};
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            float x, y;
+                            float y0, y1;
                             f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * e + 2 * z]),
                                                      __uint_as_float(v[4 * e + 2 * z + 1])),
                                              sk2, f2_pack(__uint_as_float(lw[2 * z]), __uint_as_float(lw[2 * z + 1]))),
-                                      x, y);
-                            x = kv_exp2(x);
-                            y = kv_exp2(y);
-                            if (!open) {
-                                const uint2 at = lds64(ls + 512u + 128u * q + 16u * e + 8u * z);
-                                const int ax = static_cast<int>(at.x), ay = static_cast<int>(at.y);
-                                if (j > ax || (a.window && j <= ax - a.window)) x = 0.f;
-                                if (j > ay || (a.window && j <= ay - a.window)) y = 0.f;
-                            }
-                            sum2[z] = f2_add(sum2[z], f2_pack(x, y));
+                                      y0, y1);
+                            x[4 * e + 2 * z] = kv_exp2(y0);
+                            x[4 * e + 2 * z + 1] = kv_exp2(y1);
                         }
                     }
+                    if (!open) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int at = static_cast<int>(lds32(ls + 512u + 128u * q + 4u * e));
+                            if (j > at || (a.window && j <= at - a.window)) x[e] = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(x[2 * e], x[2 * e + 1]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -239,6 +245,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
         const int ct = tid - 256, un = ct % UPR, rb = (ct / UPR) ^ (un >> 2);
         const int ucol = un * 16 < d ? un * 16 : 0;  // columns beyond head_dim meet zeros of Q
         const int ch = ct % CPR;
+        const int step_r = QSTEP % a.group;
+        const int64_t step = QSTEP / a.group * a.q_stride + static_cast<int64_t>(step_r) * d;
+        const int64_t wrap = a.q_stride - static_cast<int64_t>(a.group) * d;  // to the next token's head 0
         int t = 0;
         bool ok = true;
         // a row tile's copies arrive while the next one's are issued
@@ -297,17 +306,26 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
                 if (!ok) break;
                 const int r0 = r_lo + i * 128;
                 const uint32_t q0 = sbase + G::off_q + st * G::tile;
-#pragma unroll 8
-                for (int rr = ct / CPR; rr < 128; rr += QSTEP) {
-                    const int row = r0 + rr;
-                    uint32_t dst = q0 + (ch >> 3) * 16384u + rr * 128u +
-                                   (static_cast<uint32_t>((ch & 7) ^ (rr & 7)) << 4);
-                    if (row < r_hi && ch * 8 < d) {
-                        const int tok = row / a.group;
-                        kv_cp16(dst, a.q + (first + tok) * a.q_stride +
-                                         static_cast<int64_t>(h * a.group + row - tok * a.group) * d + ch * 8);
-                    } else {
+                // row by row of this thread's: QSTEP rows on are step_t tokens and step_r heads
+                const int tok0 = (r0 + ct / CPR) / a.group;
+                int rem = r0 + ct / CPR - tok0 * a.group;
+                const uint16_t* src = a.q + (first + tok0) * a.q_stride +
+                                      static_cast<int64_t>(h * a.group + rem) * d + ch * 8;
+                const uint32_t dst0 = q0 + (ch >> 3) * 16384u + (ct / CPR) * 128u;
+#pragma unroll
+                for (int x = 0; x < 128 / QSTEP; ++x) {
+                    const int rr = ct / CPR + x * QSTEP;
+                    const uint32_t dst = dst0 + x * QSTEP * 128u +
+                                         (static_cast<uint32_t>((ch & 7) ^ (rr & 7)) << 4);
+                    if (r0 + rr < r_hi && ch * 8 < d)
+                        kv_cp16(dst, src);
+                    else
                         sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+                    src += step;
+                    rem += step_r;
+                    if (rem >= a.group) {
+                        rem -= a.group;
+                        src += wrap;
                     }
                 }
                 {
