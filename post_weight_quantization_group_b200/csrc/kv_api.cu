@@ -189,12 +189,12 @@ q4_status run_mass(const KvMass& a, int64_t grid, cudaStream_t st) {
                      1, true, st, a);
 }
 
-template <bool BF16>
+template <bool BF16, bool PAIRS>
 q4_status run_append(const KvAppend& a, dim3 grid, cudaStream_t st) {
     switch (team_size(a.pool.d)) {
-        case 8: return launch_ex(kv_append_kernel<BF16, 8>, grid, dim3(256), 0, 1, true, st, a);
-        case 16: return launch_ex(kv_append_kernel<BF16, 16>, grid, dim3(256), 0, 1, true, st, a);
-        default: return launch_ex(kv_append_kernel<BF16, 32>, grid, dim3(256), 0, 1, true, st, a);
+        case 8: return launch_ex(kv_append_kernel<BF16, 8, PAIRS>, grid, dim3(256), 0, 1, true, st, a);
+        case 16: return launch_ex(kv_append_kernel<BF16, 16, PAIRS>, grid, dim3(256), 0, 1, true, st, a);
+        default: return launch_ex(kv_append_kernel<BF16, 32, PAIRS>, grid, dim3(256), 0, 1, true, st, a);
     }
 }
 
@@ -272,7 +272,6 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
     a.tokens = tokens;
     a.q_heads = q_heads;
     a.rot = rot_dim;
-    a.interleaved = interleaved;
     a.eps = eps;
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
@@ -285,7 +284,9 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tokens, 8LL * sms)),
                     static_cast<unsigned>((heads + a.heads_per_cta - 1) / a.heads_per_cta));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return cache->dtype == Q4_BF16 ? run_append<true>(a, grid, st) : run_append<false>(a, grid, st);
+    if (cache->dtype == Q4_BF16)
+        return interleaved ? run_append<true, true>(a, grid, st) : run_append<true, false>(a, grid, st);
+    return interleaved ? run_append<false, true>(a, grid, st) : run_append<false, false>(a, grid, st);
 }
 
 q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t* slots, int64_t tokens,

@@ -93,7 +93,7 @@ struct KvAppend {
     const int32_t* positions;
     const float* inv_freq;  // [rot / 2]
     int64_t tokens;
-    int q_heads, rot, interleaved, heads_per_cta;
+    int q_heads, rot, heads_per_cta;
     float eps;
     unsigned* status;
 };
@@ -111,9 +111,12 @@ template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = static_cast<uint32_t>(cache_bits<BF16>(v[2 * i])) |
-               (static_cast<uint32_t>(cache_bits<BF16>(v[2 * i + 1])) << 16);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -121,16 +124,19 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // of TS lanes one head, a lane eight consecutive elements (d <= 8 TS), so the
 // norm and the row maximum are shuffles and nothing of a row is read twice.
 // The heads run q, k, v.  The angles of a token are the same for all of its
-// heads and are computed once per CTA:
+// heads: they are computed once per CTA while the token before is worked on, and
+// a lane keeps its eight of them in registers:
 //   pos * inv_freq in turns, reduced in fp64 (53 bits keep a position of 2^31
 //   within 2e-7 of a turn), then sine and cosine of the remainder in fp32.
 // K is quantized from its fp32 rotated value: a rounding to the cache type in
-// between would add an error of its own.  Bound by memory: every element is
-// read and written once.
-template <bool BF16, int TS>
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppend a) {
+// between would add an error of its own.  Bound by memory for long prompts
+// (every element is read and written once) with the instruction rate close
+// behind, so a warp whose heads are all queries has a path of its own, without
+// the quantization and without branches.  PAIRS: interleaved rotation.
+template <bool BF16, int TS, bool PAIRS>
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppend a) {
     constexpr int TEAMS = 256 / TS;
-    __shared__ float2 cs[128];
+    __shared__ float2 cs[2][128];
     grid_launch_dependents();
     grid_dependency_wait();
     const KvPool& c = a.pool;
@@ -140,102 +146,136 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     const bool on = sub * 8 < d;
     const int h_beg = blockIdx.y * a.heads_per_cta;
     const int h_end = min(h_beg + a.heads_per_cta, a.q_heads + 2 * c.heads);
+    const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;
     uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
     if (on && a.q_norm) wq = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + sub);
     if (on && a.k_norm) wk = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + sub);
+    const float inv_d = 1.f / static_cast<float>(d);
 
     auto load = [&](int64_t tok, int h) -> uint4 {
         if (!on || h >= h_end) return make_uint4(0, 0, 0, 0);
         const uint16_t* p;
         if (h < a.q_heads)
-            p = a.q + tok * a.q_stride + static_cast<int64_t>(h) * d;
+            p = a.q + tok * a.q_stride + h * d;
         else if (h < a.q_heads + c.heads)
-            p = a.k + tok * a.k_stride + static_cast<int64_t>(h - a.q_heads) * d;
+            p = a.k + tok * a.k_stride + (h - a.q_heads) * d;
         else
-            p = a.v + tok * a.v_stride + static_cast<int64_t>(h - a.q_heads - c.heads) * d;
+            p = a.v + tok * a.v_stride + (h - a.q_heads - c.heads) * d;
         return *reinterpret_cast<const uint4*>(p + sub * 8);
     };
-
-    for (int64_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x) {
-        uint4 nxt = load(tok, h_beg + team);
+    auto angles = [&](int64_t tok, float2* to) {
         for (int i = threadIdx.x; i < half; i += 256) {
             double t = static_cast<double>(__ldg(a.positions + tok)) *
                        static_cast<double>(__ldg(a.inv_freq + i)) * 0.15915494309189533577;
             t -= rint(t);
             float s, co;
             sincospif(static_cast<float>(2.0 * t), &s, &co);
-            cs[i] = make_float2(co, s);
+            to[i] = make_float2(co, s);
         }
-        const int64_t slot = __ldg(a.slots + tok);
-        int64_t page = 0;
-        int off = 0;
-        bool write = slot >= 0;
-        if (write) {
-            page = slot / c.ps;
-            off = static_cast<int>(slot - page * c.ps);
-            if (page >= c.pages) {
-                write = false;
-                if (threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
+    };
+
+    int64_t tok = blockIdx.x;
+    if (tok >= a.tokens) return;
+    uint4 nxt = load(tok, h_beg + team);
+    angles(tok, cs[0]);
+    int64_t slot = __ldg(a.slots + tok);
+    __syncthreads();
+    for (int buf = 0; tok < a.tokens; buf ^= 1) {
+        const int64_t next = tok + gridDim.x;
+        // where the token's key and value go
+        const int64_t page = shift >= 0 ? slot >> shift : slot / c.ps;
+        const int off = static_cast<int>(slot - page * c.ps);
+        const bool write = slot >= 0 && page < c.pages;
+        if (slot >= 0 && !write && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
+        if (next < a.tokens) {
+            slot = __ldg(a.slots + next);
+            angles(next, cs[buf ^ 1]);
+        }
+        // This lane's part of the rotation: v' = v f.x + partner f.y, element by element, or
+        // pair by pair; (1, 0) where nothing turns.
+        float2 f[PAIRS ? 4 : 8];
+        const bool lo = sub < hl;
+        const int peer = PAIRS ? 0 : lane0 + (lo ? sub + hl : sub < 2 * hl ? sub - hl : sub);
+#pragma unroll
+        for (int i = 0; i < (PAIRS ? 4 : 8); ++i) {
+            const int at = PAIRS ? sub * 4 + i : (lo ? sub : sub - hl) * 8 + i;
+            const bool rot = PAIRS ? at < half : sub < 2 * hl;
+            f[i] = rot ? cs[buf][at] : make_float2(1.f, 0.f);
+            if (!PAIRS && lo) f[i].y = -f[i].y;
+        }
+        auto rotate = [&](float (&v)[8]) {
+            if constexpr (PAIRS) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = v[2 * i], y = v[2 * i + 1];
+                    v[2 * i] = x * f[i].x - y * f[i].y;
+                    v[2 * i + 1] = y * f[i].x + x * f[i].y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = __shfl_sync(0xFFFFFFFFu, v[i], peer);
+                    v[i] = fmaf(v[i], f[i].x, y * f[i].y);
+                }
             }
-        }
-        __syncthreads();
-        // uniform over the warp's teams, so that all lanes take part in the shuffles
-        for (int hb = h_beg; hb < h_end; hb += TEAMS) {
-            const int h = hb + team;
-            const uint4 raw = nxt;
-            nxt = load(tok, h + TEAMS);
-            const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + c.heads;
-            float v[8];
-            unpack8<BF16>(raw, v);
-            const bool norm = is_q ? a.q_norm != nullptr : !is_v && a.k_norm != nullptr;
+        };
+        auto normalize = [&](float (&v)[8], const uint4& weight) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
 #pragma unroll
             for (int o = TS / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            if (norm) {
-                float w[8];
-                unpack8<BF16>(is_q ? wq : wk, w);
-                const float r = rsqrtf(ss / static_cast<float>(d) + a.eps);
+            const float r = rsqrtf(ss * inv_d + a.eps);
+            float w[8];
+            unpack8<BF16>(weight, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+            for (int i = 0; i < 8; ++i) v[i] *= r * w[i];
+        };
+        // uniform over the warp's teams, so that all lanes take part in the shuffles
+        const uint16_t* qp = a.q + tok * a.q_stride + sub * 8;
+        uint16_t* qo = a.q_out + tok * a.qo_stride + sub * 8;
+        for (int hb = h_beg; hb < h_end; hb += TEAMS) {
+            const int h = hb + team;
+            const uint4 raw = nxt;
+            if (hb + 2 * TEAMS <= min(a.q_heads, h_end))
+                nxt = on ? *reinterpret_cast<const uint4*>(qp + (h + TEAMS) * d) : make_uint4(0, 0, 0, 0);
+            else if (hb + TEAMS < h_end)
+                nxt = load(tok, h + TEAMS);
+            else if (next < a.tokens)
+                nxt = load(next, h_beg + team);
+            float v[8];
+            unpack8<BF16>(raw, v);
+            if (hb + TEAMS <= min(a.q_heads, h_end)) {  // all queries
+                if (a.q_norm) normalize(v, wq);
+                if (half) rotate(v);
+                if (on) *reinterpret_cast<uint4*>(qo + h * d) = pack8<BF16>(v);
+                continue;
             }
-            if (a.interleaved) {
-                if (!is_v) {
+            const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + c.heads;
+            if (__any_sync(0xFFFFFFFFu, !is_v)) {
+                float u[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (sub * 8 + 2 * i < a.rot) {
-                            const float2 f = cs[sub * 4 + i];
-                            const float x = v[2 * i], y = v[2 * i + 1];
-                            v[2 * i] = x * f.x - y * f.y;
-                            v[2 * i + 1] = y * f.x + x * f.y;
-                        }
+                for (int i = 0; i < 8; ++i) u[i] = v[i];
+                const uint4 weight = is_q ? wq : wk;
+                if (a.q_norm || a.k_norm) {
+                    normalize(u, weight);
+                    if (is_q ? a.q_norm == nullptr : a.k_norm == nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = v[i];
                     }
                 }
-            } else if (half) {
-                const bool lo = sub < hl, rot = sub < 2 * hl;
-                const int peer = lane0 + (lo ? sub + hl : rot ? sub - hl : sub);
+                if (half) rotate(u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = __shfl_sync(0xFFFFFFFFu, v[i], peer);
-                    if (rot && !is_v) {
-                        const float2 f = cs[(lo ? sub : sub - hl) * 8 + i];
-                        v[i] = lo ? v[i] * f.x - y * f.y : v[i] * f.x + y * f.y;
-                    }
-                }
+                for (int i = 0; i < 8; ++i) v[i] = is_v ? v[i] : u[i];
             }
+            if (is_q && on && h < h_end) *reinterpret_cast<uint4*>(qo + h * d) = pack8<BF16>(v);
+            if (!__any_sync(0xFFFFFFFFu, !is_q && h < h_end)) continue;
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
             for (int o = TS / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            if (!on || h >= h_end) continue;
-            if (is_q) {
-                *reinterpret_cast<uint4*>(a.q_out + tok * a.qo_stride +
-                                          static_cast<int64_t>(h) * d + sub * 8) = pack8<BF16>(v);
-                continue;
-            }
-            if (!write) continue;
+            if (is_q || !on || h >= h_end || !write) continue;
             const uint16_t sbits = cache_bits<BF16>(__fdiv_rn(m, 127.0f));
             const float s = cache_value<BF16>(sbits);
             const float rs = quot_recip(s);
@@ -251,7 +291,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
             *reinterpret_cast<uint2*>(codes + sub * 8) = packed;
             if (sub == 0) (is_v ? c.vs + page * c.vs_page : c.ks + page * c.ks_page)[row] = sbits;
         }
-        __syncthreads();  // the next token overwrites the angles
+        __syncthreads();  // the next token's angles are there, and this one's are done with
+        tok = next;
     }
 }
 
