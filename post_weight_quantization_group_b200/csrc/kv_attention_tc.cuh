@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                     tmem_wait_st();
                     scx = sbase + G::off_one + (lane & 3) * 8u;
                 }
-                // One pass, 16 columns at a time, the next ones' S on its way: x = S sk + lg,
+                // One pass, 32 columns at a time, the next ones' S on its way: x = S sk + lg,
                 // p' = 2^(x - m) with the maximum known so far, their sum with 1 / sv into l. The
                 // packed p' of columns 16 q .. go over columns 8 q .. of S, which have been read.
                 // A chunk whose maximum is more than kKvLazy above m (rare after a segment's
@@ -324,94 +324,96 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 }
                 uint32_t sv[2][16];
                 read_s(0, sv[0]);
+                read_s(1, sv[1]);
 #pragma unroll 1
-                for (int q2 = 0; q2 < 8; q2 += 2) {
+                for (int q = 0; q < 8; q += 2) {  // two groups of 16 columns
+                    uint64_t x[16];
+                    tmem_wait_ld_for(sv[0]);
+                    tmem_wait_ld_for(sv[1]);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int q = q2 + z;
-                        uint32_t(&v)[16] = sv[z];
-                        tmem_wait_ld_for(v);
-                        if (z == 0 || q2 < 6) read_s(q + 1, sv[z ^ 1]);
-                        uint64_t x[8];
-                        float mx[4];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint64_t sk = lds_f2(scx + 64 * q + 32 * y);
-                            const uint64_t lg = lds_f2(scx + 512 + 64 * q + 32 * y);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t* w2 = v + 8 * (k >> 1) + 4 * y + 2 * (k & 1);
-                                x[4 * y + k] = f2_fma(f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])),
-                                                      sk, lg);
-                            }
-                        }
-                        bool grow = false;
+                    for (int y = 0; y < 4; ++y) {
+                        const uint64_t sk = lds_f2(scx + 64 * q + 32 * y);
+                        const uint64_t lg = lds_f2(scx + 512 + 64 * q + 32 * y);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            float u0, t0, u1, t1;
-                            f2_unpack(x[k], u0, t0);
-                            f2_unpack(x[4 + k], u1, t1);
-                            mx[k] = fmaxf(f_max3(u0, t0, u1), t1);
-                            grow |= mx[k] > m[k] + kKvLazy;
+                            const uint32_t* w2 = sv[y >> 1] + 8 * (k >> 1) + 4 * (y & 1) + 2 * (k & 1);
+                            x[4 * y + k] = f2_fma(f2_pack(__uint_as_float(w2[0]), __uint_as_float(w2[1])), sk, lg);
                         }
-                        if (__any_sync(0xFFFFFFFFu, grow)) {
-                            float f[4];
+                    }
+                    if (q < 6) {
+                        read_s(q + 2, sv[0]);
+                        read_s(q + 3, sv[1]);
+                    }
+                    float mx[4];
+                    bool grow = false;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
-                                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
-                                // each row of its own: what the warp's other rows do leaves it alone
-                                const float mn = mx[k] > m[k] + kKvLazy ? mx[k] : m[k];
-                                f[k] = kv_exp2(m[k] - mn);
-                                m[k] = mn;
-                                lx[k] = f2_fma(lx[k], f2_pack(f[k], f[k]), 0ull);
-                                neg_m[k] = f2_pack(-mn, -mn);
-                            }
-                            const float fr = by_lane(f);
-                            if (i > 0) {
-                                ok = warp_wait(&pv_done[half], n - 1, a.status) && ok;
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int o8 = 0; o8 < DP / 8; ++o8) {
-                                    uint32_t o[8];
-                                    tmem_ld8(to + 8 * o8, o);
-                                    tmem_wait_ld();
+                    for (int k = 0; k < 4; ++k) {
+                        float u[4], t[4];
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
-                                    tmem_st8(to + 8 * o8, o);
-                                }
-                            }
-                            tmem_wait_st();  // the earlier chunks' weights
+                        for (int y = 0; y < 4; ++y) f2_unpack(x[4 * y + k], u[y], t[y]);
+                        mx[k] = fmaxf(f_max3(f_max3(u[0], t[0], u[1]), t[1], u[2]), f_max3(t[2], u[3], t[3]));
+                        grow |= mx[k] > m[k] + kKvLazy;
+                    }
+                    if (__any_sync(0xFFFFFFFFu, grow)) {
+                        float f[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
+                            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
+                            // each row of its own: what the warp's other rows do leaves it alone
+                            const float mn = mx[k] > m[k] + kKvLazy ? mx[k] : m[k];
+                            f[k] = kv_exp2(m[k] - mn);
+                            m[k] = mn;
+                            lx[k] = f2_fma(lx[k], f2_pack(f[k], f[k]), 0ull);
+                            neg_m[k] = f2_pack(-mn, -mn);
+                        }
+                        const float fr = by_lane(f);
+                        if (i > 0) {
+                            ok = warp_wait(&pv_done[half], n - 1, a.status) && ok;
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int o8 = 0; o8 < q; ++o8) {
+                            for (int o8 = 0; o8 < DP / 8; ++o8) {
                                 uint32_t o[8];
-                                tmem_ld8(ts + 8 * o8, o);
+                                tmem_ld8(to + 8 * o8, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const __half2 h2 = *reinterpret_cast<__half2*>(&o[e]);
-                                    o[e] = kv_pack_f16(__low2float(h2) * fr, __high2float(h2) * fr);
-                                }
-                                tmem_st8(ts + 8 * o8, o);
+                                for (int e = 0; e < 8; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+                                tmem_st8(to + 8 * o8, o);
                             }
                         }
-                        uint32_t p[8];
+                        tmem_wait_st();  // the earlier groups' weights
+#pragma unroll 1
+                        for (int o8 = 0; o8 < q; ++o8) {
+                            uint32_t o[8];
+                            tmem_ld8(ts + 8 * o8, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint64_t inv = lds_f2(sc + 1024 + 64 * q + 32 * y);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float u, t;
-                                f2_unpack(f2_add(x[4 * y + k], neg_m[k]), u, t);
-                                u = kv_exp2(u);
-                                t = kv_exp2(t);
-                                lx[k] = f2_fma(f2_pack(u, t), inv, lx[k]);
-                                p[4 * (k >> 1) + 2 * y + (k & 1)] = kv_pack_f16(u, t);
+                            for (int e = 0; e < 8; ++e) {
+                                const __half2 h2 = *reinterpret_cast<__half2*>(&o[e]);
+                                o[e] = kv_pack_f16(__low2float(h2) * fr, __high2float(h2) * fr);
                             }
+                            tmem_st8(ts + 8 * o8, o);
                         }
-                        tmem_st_pairs8(ts + 8 * q, p);
-                        tmem_st_pairs8(ts + 8 * q + (16u << 16), p + 4);
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint64_t inv = lds_f2(sc + 1024 + 64 * q + 32 * y);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float u, t;
+                            f2_unpack(f2_add(x[4 * y + k], neg_m[k]), u, t);
+                            u = kv_exp2(u);
+                            t = kv_exp2(t);
+                            lx[k] = f2_fma(f2_pack(u, t), inv, lx[k]);
+                            p[8 * (y >> 1) + 4 * (k >> 1) + 2 * (y & 1) + (k & 1)] = kv_pack_f16(u, t);
+                        }
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        tmem_st_pairs8(ts + 8 * (q + z), p + 8 * z);
+                        tmem_st_pairs8(ts + 8 * (q + z) + (16u << 16), p + 8 * z + 4);
                     }
                 }
 #pragma unroll
