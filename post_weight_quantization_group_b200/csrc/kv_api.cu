@@ -484,9 +484,10 @@ q4_status kv_evict_int8_paged(const kv_paged_int8* cache, float* mass, int64_t m
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int units = batch->seqs * cache->heads;
     const int sms = sm_count(current_device());
-    // CTAs of a unit: as many (up to 8) as leave each 2048 tokens and the device's SMs not full twice
+    // CTAs of a unit (each takes an SM): up to 8 that are all resident at once, with 2048
+    // tokens or more each
     int parts = 1;
-    while (parts < 8 && units * parts < sms && cap / (2 * parts) >= 2048) parts *= 2;
+    while (parts < 8 && units * parts * 2 <= sms && cap / (2 * parts) >= 2048) parts *= 2;
     const int vec = (cache->page_size % 4) == 0 && aligned(mass, 16) && (mass_stride % 4) == 0;
     if (static_cast<int64_t>(units) * parts > INT32_MAX) return Q4_ERR_SHAPE;
     s = launch_ex(kv_evict_select_kernel, dim3(static_cast<unsigned>(units * parts)), dim3(kEvThreads), 0,
