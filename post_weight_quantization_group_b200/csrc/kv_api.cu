@@ -114,8 +114,11 @@ struct AttnPlan {
     int rows;             // rows of a unit
     int lead;             // what beginning and ending a unit costs, in tiles
     int64_t ctas;         // at most so many
-    size_t slot, bytes;   // floats of a partial slot; workspace bytes
+    size_t bytes;         // of workspace
 };
+
+// CTAs of the few-rows kernel that the device holds at once.
+int64_t rows_ctas(int dp, int nr, int sms) { return (dp * nr > 128 ? 1LL : 2LL) * sms; }
 
 AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
     AttnPlan p{};
@@ -124,9 +127,11 @@ AttnPlan attn_plan(int d, int64_t group, int64_t max_new, int sms) {
     p.nr = max_new * group <= 8 ? 1 : 2;
     p.rows = p.tc ? kTcaRows : 8 * p.nr;
     p.lead = p.tc ? 1 : kKvLead;
-    p.ctas = static_cast<int64_t>(p.tc || dp * p.nr > 128 ? 1 : 2) * sms;
-    p.slot = static_cast<size_t>(p.rows) * (dp + 2);
-    p.bytes = kWsCounterBytes + 2 * static_cast<size_t>(p.ctas) * p.slot * 4;
+    // the other kernel's parts never need more than the tensor-core one's, which a mixed
+    // batch takes after it
+    p.ctas = p.tc ? sms : rows_ctas(dp, p.nr, sms);
+    const size_t slot = static_cast<size_t>(p.rows) * (dp + 2);  // floats of a partial slot
+    p.bytes = kWsCounterBytes + 2 * static_cast<size_t>(p.ctas) * slot * 4;
     return p;
 }
 
@@ -339,7 +344,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {p.rows, kKvTile, group, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), p.lead};
+              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), p.lead, 0, INT32_MAX};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.out = static_cast<uint16_t*>(out);
@@ -352,10 +357,27 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsCounterBytes);
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
-    const int64_t grid = attn_grid(a, p.ctas);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return cache->dtype == Q4_BF16 ? dispatch_attention<true>(a, p, grid, st)
-                                   : dispatch_attention<false>(a, p, grid, st);
+    const bool bf = cache->dtype == Q4_BF16;
+    if (p.tc && batch->tokens < batch->max_new * batch->seqs) {
+        // Chunks beside decode steps: those go to the other kernel, since a tile costs the
+        // tensor-core kernel the same however few of its 256 rows are any (4 chunks of 257 and
+        // 12 single tokens over up to 8100: 183 us in one kernel).
+        AttnPlan few = p;
+        few.tc = false;
+        few.nr = group <= 8 ? 1 : 2;
+        few.ctas = rows_ctas(padded_dim(cache->head_dim), few.nr, sms);
+        KvAttn b = a;
+        b.geom.R = 8 * few.nr;
+        b.geom.lead = kKvLead;
+        b.geom.rows_hi = 8 * few.nr;
+        a.geom.rows_lo = 8 * few.nr;
+        s = bf ? dispatch_attention<true>(b, few, attn_grid(b, few.ctas), st)
+               : dispatch_attention<false>(b, few, attn_grid(b, few.ctas), st);
+        if (s != Q4_OK) return s;
+    }
+    const int64_t grid = attn_grid(a, p.ctas);
+    return bf ? dispatch_attention<true>(a, p, grid, st) : dispatch_attention<false>(a, p, grid, st);
 }
 
 q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q, int64_t q_stride,
@@ -378,7 +400,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
         k.batch = batch_of(batch, cache->page_size);
         const int nr = max_new * group <= 8 ? 1 : 2;
         k.geom = {8 * nr, kKvTile, group, cache->heads,
-                  static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), kKvLead};
+                  static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), kKvLead, 0, INT32_MAX};
         if (window >= k.batch.cap) k.geom.window = 0;  // hides nothing
         k.q = static_cast<const uint16_t*>(q);
         k.lse = const_cast<float*>(lse);  // read
@@ -419,7 +441,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {kKvTile, kKvTile, q_heads / cache->heads, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), 0};
+              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), 0, 0, INT32_MAX};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.lse = lse;

@@ -350,11 +350,14 @@ __global__ void __launch_bounds__(256)
 
 struct KvGeom {
     int R, KT, group, heads, window, lead;
+    // sequences with more than rows_lo and at most rows_hi rows; the others are left alone
+    int rows_lo, rows_hi;
 };
 
 // Row tiles of a sequence.
 __device__ __forceinline__ int kv_row_tiles(const KvGeom& g, const KvSeq& s) {
-    return (s.n * g.group + g.R - 1) / g.R;
+    const int rows = s.n * g.group;
+    return rows > g.rows_lo && rows <= g.rows_hi ? (rows + g.R - 1) / g.R : 0;
 }
 
 // Tiles [lo, lo + count) that the rows of tile rt see.
@@ -488,7 +491,7 @@ __device__ __forceinline__ void kv_next_unit(const KvBatch& bt, const KvGeom& g,
         ++w->b;
         if (w->b >= bt.seqs) return;
         *s = kv_seq(bt, w->b, status);
-    } while (s->n == 0);
+    } while (kv_row_tiles(g, *s) == 0);
 }
 
 // CTA that owns place i when T places are cut into P ranges [T p / P, T (p + 1) / P).
