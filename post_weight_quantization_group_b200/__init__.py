@@ -626,18 +626,18 @@ class KVPagedInt8:
 
     def c_struct(self) -> _CKVPaged:
         kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
-        shape = kc.shape
+        shape, rows = kc.shape, ks.shape
         if kc.dtype is not torch.int8 or vc.dtype is not torch.int8 or len(shape) != 4 or vc.shape != shape:
             raise ValueError("k_codes and v_codes must be int8 [pages, heads, page_size, head_dim]")
         dt = ks.dtype
-        if dt not in _DT or vs.dtype != dt or ks.shape != shape[:3] or vs.shape != shape[:3]:
+        if dt not in _DT or vs.dtype is not dt or rows != shape[:3] or vs.shape != rows:
             raise ValueError("k_scales and v_scales must be [pages, heads, page_size] of one 16-bit type")
         pages, heads, ps, d = shape
         _same_device(kc, ks, vc, vs)
+        n = heads * ps
         return _CKVPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                         _page_stride(kc, heads * ps * d), _page_stride(ks, heads * ps),
-                         _page_stride(vc, heads * ps * d), _page_stride(vs, heads * ps), pages,
-                         heads, ps, d, _DT[dt])
+                         _page_stride(kc, n * d), _page_stride(ks, n), _page_stride(vc, n * d),
+                         _page_stride(vs, n), pages, heads, ps, d, _DT[dt])
 
 
 def kv_paged_int8(pages: int, heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16,
@@ -655,17 +655,20 @@ def _page_stride(x: torch.Tensor, dense: int) -> int:
     page's own size, inside which nothing may lie apart."""
     if x.is_contiguous():
         return dense
-    if not x[0].is_contiguous():
-        raise ValueError("what lies inside a page, or inside a token, must be dense")
-    return x.stride(0) if x.shape[0] > 1 else dense
+    size, stride, want = x.shape, x.stride(), 1
+    for i in range(len(size) - 1, 0, -1):
+        if size[i] > 1 and stride[i] != want:
+            raise ValueError("what lies inside a page, or inside a token, must be dense")
+        want *= size[i]
+    return stride[0] if size[0] > 1 else dense
 
 
 def _same_device(first: torch.Tensor, *rest):
-    if not first.is_cuda:
+    dev = first.get_device()  # -1 on the host
+    if dev < 0:
         raise ValueError("q4 takes device tensors only")
-    dev = first.device
     for t in rest:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors of a call must be on one device")
 
 
@@ -731,6 +734,11 @@ def _head_rows(t: torch.Tensor, what: str, heads: int | None, d: int, dtype, tok
     return _page_stride(t, t.shape[1] * d)
 
 
+def _empty_as(q: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of q's shape."""
+    return torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
+
+
 def _int32(t: torch.Tensor | None, what: str, shape):
     if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
@@ -782,7 +790,7 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
     _same_device(cache.k_codes, q, k, v, slots, positions, inv_freq, q_norm, k_norm, q_out)
     with _Call(k.device, stream) as call:
         if q is not None and q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _empty_as(q)
         os_ = _head_rows(q_out, "q_out", q.shape[1], d, dt, tokens) if q is not None else 0
         st = lib.kv_append_int8_paged(
             ctypes.byref(cs), q.data_ptr() if q is not None else None, qs,
@@ -810,7 +818,7 @@ def kv_gather_int8_paged(cache: KVPagedInt8, slots: torch.Tensor, k_out: torch.T
         if k_out is None:
             k_out = cache.k_scales.new_empty(shape)
         if v_out is None:
-            v_out = cache.k_scales.new_empty(shape)
+            v_out = torch.empty_like(k_out)
         for x in (k_out, v_out):
             if x.dtype != cache.dtype or x.shape != shape or not x.is_contiguous():
                 raise ValueError("k_out and v_out must be contiguous [tokens, heads, head_dim] in the cache type")
@@ -839,7 +847,7 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     _same_device(cache.k_codes, q, block_table, seq_lens, cu_new, out, lse, workspace)
     with _Call(q.device, stream) as call:
         if out is None:
-            out = q.new_empty(q.shape)
+            out = _empty_as(q)
         if lse is None:
             lse = q.new_empty((tokens, hq), dtype=torch.float32)
         elif lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous():

@@ -208,12 +208,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
     kv_locate<kTcaThreads>(a.batch, a.geom, blockIdx.x, gridDim.x, 1, a.status, &s_loc, &T, &P, &beg,
                            &end, &w);
     const int group = a.geom.group, window = a.geom.window;
-    // a value the compiler cannot compute ahead of its use
-    auto opaque = [](uint32_t v) {
-        asm volatile("" : "+r"(v));
-        return v;
-    };
-
     if (warp < 8) {
         // ------------------------------------------------------ softmax
         const int half = warp >> 2;
@@ -655,9 +649,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             int c = 0;
             uint32_t n[2] = {0, 0};
             // A descriptor's low word is an address and grows by constants from step to
-            // step.  `opaque` keeps the compiler from computing the loop's 24 descriptors
-            // ahead of it and spilling them: with shared memory this full there is next to
-            // no L1, and each reload took 350 cycles (a tile 17,000 instead of 2,900).
+            // step.  (Where this thread had 40 registers the loop's descriptors were computed
+            // ahead of it and spilled: with shared memory this full there is next to no L1, each
+            // reload took 350 cycles, and a tile 17,000.)
             auto desc = [](uint32_t lo, uint32_t hi) {
                 uint64_t v;
                 asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
@@ -667,9 +661,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
             const uint32_t klo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32);
             const uint32_t nlo = static_cast<uint32_t>(nd), nhi = static_cast<uint32_t>(nd >> 32);
             auto issue_s = [&](int half, int st) {
-                const uint32_t q = opaque(klo + ((G::off_q + half * G::tile) >> 4));
-                const uint32_t k = opaque(klo + ((G::off_k + st * G::tile) >> 4));
-                const uint32_t ds = opaque(tbase + half * 128);
+                const uint32_t q = klo + ((G::off_q + half * G::tile) >> 4);
+                const uint32_t k = klo + ((G::off_k + st * G::tile) >> 4);
+                const uint32_t ds = tbase + half * 128;
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
@@ -678,8 +672,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 umma_commit(&s_full[half]);
             };
             auto issue_pv = [&](int half, int st, bool add) {
-                const uint32_t v = opaque(nlo + ((G::off_v + st * G::tile) >> 4));
-                const uint32_t ds = opaque(tbase + kColO + half * DP), pa = opaque(tbase + half * 128);
+                const uint32_t v = nlo + ((G::off_v + st * G::tile) >> 4);
+                const uint32_t ds = tbase + kColO + half * DP, pa = tbase + half * 128;
 #pragma unroll
                 for (int kk = 0; kk < kTcaKT / 16; ++kk)
                     umma_f16_ts(ds, pa + kk * 8, desc(v + kk * 128u, nhi), kIdescO,
