@@ -520,9 +520,11 @@ Q4_API q4_status kv_dequant_int4(const uint8_t* packed, const void* scales, int6
  * drop is the subject of "LLM 后训练量化深度实战" (ybb.press) section 七 (sink
  * tokens, recent tokens).
  *
- * Arrays on the device (lengths, tables, slots) are read by the kernels; what
- * is out of range in them is brought into range, nothing is read or written
- * out of bounds, and the next q4_sync_status returns Q4_ERR_INVALID_ARG.
+ * Arrays on the device (lengths, tables, slots) are read by the kernels.
+ * Where they are out of range nothing is read out of bounds (some other row
+ * of the pool is read instead, so results of that sequence mean nothing),
+ * nothing is written to a page or slot that was not named, and the next
+ * q4_sync_status returns Q4_ERR_INVALID_ARG.
  */
 typedef struct kv_paged_int8 {
     int8_t* k_codes;  /* [pages, heads, page_size, head_dim], 16-byte aligned */
@@ -548,7 +550,7 @@ typedef struct kv_batch {
     const int32_t* cu_new;      /* [seqs + 1]: rows cu_new[b] .. cu_new[b+1] - 1 of q are sequence
                                    b's new tokens, its last ones; NULL: row b is sequence b's one
                                    new token */
-    int64_t table_width;        /* table_width * page_size < 2^31 - 2^16 */
+    int64_t table_width;        /* table_width * page_size <= 2^30 */
     int64_t tokens;             /* rows of q; rows that no sequence names are left as they are */
     int64_t max_new;            /* >= 1: the most new tokens of a sequence.  Only the choice of
                                    kernel depends on it. */
@@ -611,14 +613,14 @@ Q4_API q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t*
  *   q          [tokens, q_heads, head_dim] in the cache type, rows q_stride apart
  *   out        the same shape, rows out_stride apart; must not overlap q
  *   lse        fp32 [tokens, q_heads], or NULL
- *   scale      any finite value
+ *   scale      finite, of any sign; scaled scores have to stay inside fp32's range
  *   workspace  kv_attention_workspace_bytes(head_dim, q_heads, heads, max_new)
  *              bytes, 256-byte aligned, its first 256 KiB zero-filled before the first use (a
  *              call leaves them so); the INT4 products' workspace serves too if large enough.
  *              Calls that may overlap on the GPU need separate buffers.
  * The work is divided on the device by the lengths found there, so the call
  * can be captured and replayed with other lengths; the result does not depend on
- * timing.  tokens * q_heads < 2^31 - 2^16.
+ * timing.  tokens * q_heads <= 2^30.
  */
 Q4_API size_t kv_attention_workspace_bytes(int32_t head_dim, int32_t q_heads, int32_t kv_heads,
                                            int64_t max_new);

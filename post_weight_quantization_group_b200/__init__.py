@@ -459,7 +459,10 @@ def bf16_gemv_ref_bw(W: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = 
 
 def q4_sync_status(stream=None) -> int:
     """Synchronize ``stream`` and return (and clear) the device status."""
-    return load_library().q4_sync_status(_stream(stream))
+    status = load_library().q4_sync_status(_stream(stream))
+    if status == Q4_ERR_TIMEOUT:
+        _stream_workspaces.clear()  # their counters may not be zero
+    return status
 
 
 def q4_selftest_wait_timeout(limit_ns: int, stream=None) -> int:

@@ -23,8 +23,8 @@ namespace {
 
 using namespace q4dev;
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 16);  // 32-bit row arithmetic of the kernels
-constexpr int64_t kMaxLen = (int64_t(1) << 31) - (1 << 16);   // and of token indices
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // 32-bit arithmetic on rows,
+constexpr int64_t kMaxLen = int64_t(1) << 30;   // and on tokens less a window less new tokens
 
 q4_status check_pool(const kv_paged_int8* c) {
     if (!c) return Q4_ERR_INVALID_ARG;
@@ -344,7 +344,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {p.rows, kKvTile, group, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), p.lead, 0, INT32_MAX};
+              static_cast<int>(std::min<int64_t>(window, kMaxLen)), p.lead, 0, INT32_MAX};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.out = static_cast<uint16_t*>(out);
@@ -359,7 +359,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     if (!a.status) return Q4_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = cache->dtype == Q4_BF16;
-    if (p.tc && batch->tokens < batch->max_new * batch->seqs) {
+    if (p.tc && batch->tokens < max_new * batch->seqs) {
         // Chunks beside decode steps: those go to the other kernel, since a tile costs the
         // tensor-core kernel the same however few of its 256 rows are any (4 chunks of 257 and
         // 12 single tokens over up to 8100: 183 us in one kernel).
@@ -400,7 +400,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
         k.batch = batch_of(batch, cache->page_size);
         const int nr = max_new * group <= 8 ? 1 : 2;
         k.geom = {8 * nr, kKvTile, group, cache->heads,
-                  static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), kKvLead, 0, INT32_MAX};
+                  static_cast<int>(std::min<int64_t>(window, kMaxLen)), kKvLead, 0, INT32_MAX};
         if (window >= k.batch.cap) k.geom.window = 0;  // hides nothing
         k.q = static_cast<const uint16_t*>(q);
         k.lse = const_cast<float*>(lse);  // read
@@ -441,7 +441,7 @@ q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q
     a.pool = pool_of(cache);
     a.batch = batch_of(batch, cache->page_size);
     a.geom = {kKvTile, kKvTile, q_heads / cache->heads, cache->heads,
-              static_cast<int>(std::min<int64_t>(window, INT32_MAX / 2)), 0, 0, INT32_MAX};
+              static_cast<int>(std::min<int64_t>(window, kMaxLen)), 0, 0, INT32_MAX};
     if (window >= a.batch.cap) a.geom.window = 0;  // hides nothing
     a.q = static_cast<const uint16_t*>(q);
     a.lse = lse;

@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             p.vc = p.kc;
             p.vs = p.ks;
             if constexpr (MASS) {
-                p.vs = page * a.mass_page + row;
+                // -1: not added
+                p.vs = entry >= 0 && entry < c.pages ? static_cast<int64_t>(page * a.mass_page + row) : -1;
             } else if (!same) {
                 p.vc = page * c.vc_page + static_cast<uint64_t>(row) * d;
                 p.vs = page * c.vs_page + row;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         }
                     }
                     b.ks += rs;
-                    b.vs += rs;
+                    if (!MASS || b.vs >= 0) b.vs += rs;
                 } else {
 #pragma unroll 1
                     for (int x = 0; x < Ring::copies; ++x) {
@@ -435,7 +436,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                     sum[f] += __shfl_xor_sync(0xFFFFFFFFu, sum[f], 2);
                     if (t == 0 && j0 + g + 8 * f < seq.len) {
                         const uint2 o = lds64(scs + g * 4u + 64u + 64u * f);
-                        atomicAdd(a.mass + ((static_cast<int64_t>(o.y) << 32) | o.x), sum[f]);
+                        const int64_t to = static_cast<int64_t>((static_cast<uint64_t>(o.y) << 32) | o.x);
+                        if (to >= 0) atomicAdd(a.mass + to, sum[f]);
                     }
                 }
                 continue;

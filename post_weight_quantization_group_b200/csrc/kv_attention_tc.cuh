@@ -122,10 +122,25 @@ __device__ __forceinline__ void tca_store16(uint32_t tile, int row, int u, const
     sts128(base + (at ^ 16u), make_uint4(o[4], o[5], o[6], o[7]));
 }
 
+// mbar_wait_bounded without a suspend time in its polls.
+__device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, unsigned* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
 // A warp's bounded wait, with one outcome for all of its lanes: a wait that
 // ran out must not part the lanes of a warp that goes on to collective steps.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, status, kWaitLimitNs));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_poll(bar, parity & 1u, status));
 }
 
 template <bool BF16, int DP>
@@ -681,7 +696,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 umma_commit(&pv_done[half]);
             };
             auto wait = [&](uint64_t* b, uint32_t ph) {
-                if (ok) ok = mbar_wait_bounded(b, ph & 1u, a.status, kWaitLimitNs);
+                if (ok) ok = mbar_wait_poll(b, ph & 1u, a.status);
                 tc_fence_after();
                 return ok;
             };

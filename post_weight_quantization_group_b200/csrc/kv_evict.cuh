@@ -286,9 +286,10 @@ __device__ __forceinline__ int kv_evict_src(const KvEvict& a, int b, int h, int 
     return len <= a.budget ? i
                            : __ldg(a.src + (static_cast<int64_t>(b) * a.pool.heads + h) * a.budget + i);
 }
+// Its page among the destination's, or -1: what has no page is not moved.
 __device__ __forceinline__ int64_t kv_evict_dst_page(const KvEvict& a, int b, int i) {
-    return kv_page(a.pool, __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_width + i / a.pool.ps),
-                   a.status);
+    const int32_t e = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_width + i / a.pool.ps);
+    return kv_valid_page(a.pool, e, a.status) ? e : -1;
 }
 
 // Destination pages apart from the source pages: every kept row on its own.  A
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(256) kv_evict_copy_kernel(const __grid_constan
             const int j = kv_evict_src(a, b, h, i, len);
             const int64_t sp = kv_page(c, kv_entry(a.batch, b, j / c.ps), a.status);
             const int64_t dp = kv_evict_dst_page(a, b, i);
+            if (dp < 0) continue;
             const int64_t sr = kv_row(c, h, j % c.ps), dr = kv_row(c, h, i % c.ps);
             if (sub * 16 < d) {
                 const uint4 k = *reinterpret_cast<const uint4*>(c.kc + sp * c.kc_page + sr * d + sub * 16);
@@ -347,8 +349,9 @@ __global__ void __launch_bounds__(256) kv_evict_inplace_kernel(const __grid_cons
             const int i = i0 + threadIdx.x;
             int j = i;
             if (i < kept) j = __ldg(a.src + static_cast<int64_t>(u) * a.budget + i);
-            const bool move = i < kept && j > i;
-            int64_t sp = 0, dp = 0, sr = 0, dr = 0;
+            const int64_t dp = i < kept && j > i ? kv_evict_dst_page(a, b, i) : -1;
+            const bool move = dp >= 0;
+            int64_t sp = 0, sr = 0, dr = 0;
             uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
             const bool wide = piece < 2 * cols;
             const int col = (piece < cols ? piece : piece - cols) * 32;
@@ -356,7 +359,6 @@ __global__ void __launch_bounds__(256) kv_evict_inplace_kernel(const __grid_cons
             const int64_t stride = piece < cols ? c.kc_page : c.vc_page;
             if (move) {
                 sp = kv_page(c, kv_entry(a.batch, b, j / c.ps), a.status);
-                dp = kv_evict_dst_page(a, b, i);
                 sr = kv_row(c, h, j % c.ps);
                 dr = kv_row(c, h, i % c.ps);
                 if (wide) {

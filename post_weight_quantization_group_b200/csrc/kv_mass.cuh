@@ -113,11 +113,14 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
         uint32_t kf[DP / 16][4];
         float sk[2];
         int64_t page[2], row[2];
+        bool named[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int j = j0 + g + 8 * e;
             const bool in = j < seq.len;
-            page[e] = in ? kv_page(c, kv_entry(a.batch, b, j / c.ps), a.status) : 0;
+            const int32_t entry = in ? kv_entry(a.batch, b, j / c.ps) : 0;
+            page[e] = kv_page(c, entry, a.status);
+            named[e] = in && entry >= 0 && entry < c.pages;
             row[e] = in ? kv_row(c, h, j % c.ps) : 0;
             const int8_t* p = c.kc + page[e] * c.kc_page + row[e] * d;
 #pragma unroll
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
         for (int f = 0; f < 2; ++f) {
             sum[f] += __shfl_xor_sync(0xFFFFFFFFu, sum[f], 1);
             sum[f] += __shfl_xor_sync(0xFFFFFFFFu, sum[f], 2);
-            if (t == 0 && j0 + g + 8 * f < seq.len)
+            if (t == 0 && named[f])
                 atomicAdd(a.mass + page[f] * a.mass_page + row[f], sum[f]);
         }
     }

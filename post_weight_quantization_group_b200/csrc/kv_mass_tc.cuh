@@ -145,12 +145,14 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
             const volatile TcmUnit& g = units[u % kTcmUnits];
             const int tiles = g.tiles, j = g.j0 + key;
             if (tiles == 0) break;
-            const bool live = j < g.len;
+            bool live = j < g.len;
             float sk = 0.f;
             int64_t place = 0;
             if (live) {
                 const int e = j / a.pool.ps;
-                const int64_t page = kv_page(a.pool, kv_entry(a.batch, g.b, e), a.status);
+                const int32_t entry = kv_entry(a.batch, g.b, e);
+                live = kv_valid_page(a.pool, entry, a.status);  // else there is nothing to add to
+                const int64_t page = live ? entry : 0;
                 const int64_t row = kv_row(a.pool, g.h, j - e * a.pool.ps);
                 sk = cache_value<BF16>(__ldg(a.pool.ks + page * a.pool.ks_page + row)) * a.scale_log2;
                 place = page * a.mass_page + row;
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_free[u % kTcmUnits]);
         }
+        kv_cp_wait<0>();  // none in flight at the exit, whatever ended the loop
     } else if (warp == 12 && lane == 0) {
         // -------------------------------------------------------- MMA issue
         auto opaque = [](uint32_t v) {
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
         const uint32_t klo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32);
         bool ok = true;
         auto wait = [&](uint64_t* b, uint32_t ph) {
-            if (ok) ok = mbar_wait_bounded(b, ph & 1u, a.status, kWaitLimitNs);
+            if (ok) ok = mbar_wait_poll(b, ph & 1u, a.status);
             tc_fence_after();
             return ok;
         };

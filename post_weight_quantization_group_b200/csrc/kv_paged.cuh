@@ -73,12 +73,14 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int i, unsigned* statu
 __device__ __forceinline__ int32_t kv_entry(const KvBatch& b, int i, int e) {
     return __ldg(b.table + static_cast<int64_t>(i) * b.width + e);
 }
+__device__ __forceinline__ bool kv_valid_page(const KvPool& c, int32_t entry, unsigned* status) {
+    if (entry >= 0 && entry < c.pages) return true;
+    atomicOr(status, kStatusBadIndex);
+    return false;
+}
+// For reads; nothing is written to a page that was not named.
 __device__ __forceinline__ int64_t kv_page(const KvPool& c, int32_t entry, unsigned* status) {
-    if (entry < 0 || entry >= c.pages) {
-        atomicOr(status, kStatusBadIndex);
-        return entry < 0 ? 0 : c.pages - 1;
-    }
-    return entry;
+    return kv_valid_page(c, entry, status) ? entry : entry < 0 ? 0 : c.pages - 1;
 }
 
 // ---------------------------------------------------------------- append

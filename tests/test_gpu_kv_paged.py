@@ -337,6 +337,38 @@ def test_attention_out_of_range_arrays(new):
         _sync_ok()
 
 
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("new", [1, 20])
+def test_bad_pages_are_not_written(d, new):
+    """A page that is none gets no mass and no evicted row; the rest is as without it."""
+    c = _Case([(200, new), (90, 1)], 8, 2, d, 16, BF, seed=12)
+    _, lse = c.attention()
+    zero = torch.zeros(c.cache.k_scales.shape, device="cuda")
+    args = (c.cache, c.q, lse)
+    want = q4.kv_attention_mass_int8_paged(*args, zero.clone(), c.table, c.len_t, c.cu_t, max_new=c.max_new)
+    _sync_ok()
+    for bad in (-1, c.cache.k_codes.shape[0]):
+        page = int(c.table[0, 4])
+        table = c.table.clone()
+        table[0, 4] = bad
+        got = q4.kv_attention_mass_int8_paged(*args, zero.clone(), table, c.len_t, c.cu_t, max_new=c.max_new)
+        assert q4.q4_sync_status() == q4.Q4_ERR_INVALID_ARG
+        expect = want.clone()
+        expect[page] = 0
+        assert torch.equal(got, expect)
+    big = _pool(40, 2, 16, d, BF, 5)
+    mass = torch.rand(40, 2, 16, generator=_gen(1), device="cuda")
+    before = [x.clone() for x in (big.k_codes, big.v_codes, big.k_scales, big.v_scales, mass)]
+    src = _cuda32([list(range(13))])
+    for bad in (-7, 40):
+        q4.kv_evict_int8_paged(big, mass, src, _cuda32([200]), 48, recent=4,
+                               dst_table=_cuda32([[20, bad, 22]]))
+        assert q4.q4_sync_status() == q4.Q4_ERR_INVALID_ARG
+        for x, y in zip((big.k_codes, big.v_codes, big.k_scales, big.v_scales, mass), before):
+            keep = [p for p in range(40) if p not in (20, 22)]
+            assert torch.equal(x[keep], y[keep])
+
+
 def test_attention_far_pages():
     """Codes beyond 2^32 bytes of a pool."""
     ps, hk, d = 128, 8, 128

@@ -97,8 +97,8 @@ def test_gather_faults(lib):
 
 
 BATCH_FAULTS = [
-    (dict(seqs=-1), "SHAPE"), (dict(table_width=-1), "SHAPE"), (dict(table_width=2 ** 28), "SHAPE"),
-    (dict(tokens=-1), "SHAPE"), (dict(max_new=0), "SHAPE"), (dict(tokens=2 ** 30), "SHAPE"),
+    (dict(seqs=-1), "SHAPE"), (dict(table_width=-1), "SHAPE"), (dict(table_width=2 ** 27), "SHAPE"),
+    (dict(tokens=-1), "SHAPE"), (dict(max_new=0), "SHAPE"), (dict(tokens=2 ** 29), "SHAPE"),
     (dict(seq_lens=None), "INVALID_ARG"), (dict(block_table=None), "INVALID_ARG"),
     (dict(seq_lens=A + 2), "ALIGNMENT"), (dict(cu_new=A + 1), "ALIGNMENT"),
 ]
