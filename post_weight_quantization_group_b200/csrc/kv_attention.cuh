@@ -29,6 +29,10 @@
 // first, which is exact for every element above 2^-31 of the row's largest,
 // and below that within 2^-40 of it: finer than the fp32 sums.
 //
+// Measured (B200, 64 query heads over 8 of 128): one token over 131,071, 65 us
+// = 4.2 TB/s, of which the loop takes 45 (6.0 TB/s); 32 ragged sequences of up
+// to 8192, 66 us; one of 1001 (32 heads), 9.5 us.
+//
 // Work split: kv_paged.cuh (equal ranges of 128-token tiles over the CTAs; a
 // warp takes 16 tokens of each tile).  The warps of a CTA keep their own
 // maxima and sums and are joined at the end of a segment; a unit that

