@@ -707,3 +707,84 @@ def test_decode_loop():
     for _ in range(3):
         step([1, 1])
     step([5, 20])
+
+
+class _Step:
+    """A decode step's buffers: everything the operators read that changes."""
+
+    def __init__(self, seed):
+        g = _gen(seed)
+        self.hq, self.hk, self.d, self.ps = 16, 2, 128, 16
+        self.cache = _pool(30, self.hk, self.ps, self.d, BF, seed)
+        self.mass = torch.rand(30, self.hk, self.ps, generator=g, device="cuda")
+        self.table = _cuda32([list(range(10)), list(range(10, 20)), list(range(20, 30))])
+        self.lens = _cuda32([0, 0, 0])
+        self.slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+        self.pos = _cuda32([0, 0, 0])
+        self.qkv = torch.zeros(3, self.hq + 2 * self.hk, self.d, dtype=BF, device="cuda")
+        self.inv = (10000.0 ** (-torch.arange(0, self.d, 2, device="cuda").double() / self.d)).float()
+
+    def set(self, i):
+        lens = [41 + i, 0, 150 + i]  # the middle row is padding: no cached token, no slot
+        self.lens.copy_(_cuda32(lens))
+        self.slots.copy_(torch.tensor([(n - 1) // 16 * 16 + b * 160 + (n - 1) % 16 if n else -1
+                                       for b, n in enumerate(lens)], device="cuda"))
+        self.pos.copy_(_cuda32([max(n - 1, 0) for n in lens]))
+        self.qkv.copy_(torch.randn(self.qkv.shape, generator=_gen(100 + i), device="cuda"))
+
+    def run(self, **kw):
+        q = q4.kv_append_int8_paged(self.cache, self.qkv[:, :self.hq], self.qkv[:, self.hq:self.hq + self.hk],
+                                    self.qkv[:, self.hq + self.hk:], self.slots, self.pos, self.inv, **kw)
+        out, lse = q4.kv_attention_int8_paged(self.cache, q, self.table, self.lens, **kw)
+        q4.kv_attention_mass_int8_paged(self.cache, q, lse, self.mass, self.table, self.lens, **kw)
+        return out, lse
+
+    def state(self):
+        c = self.cache
+        return [c.k_codes, c.k_scales, c.v_codes, c.v_scales, self.mass]
+
+
+def test_captured_decode_steps():
+    """A step captured once and replayed with other lengths, slots and inputs, a
+    padding row among them, against the same steps run one by one."""
+    a, b = _Step(50), _Step(50)
+    a.set(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = a.run()
+    for i in range(4):
+        a.set(i)
+        b.set(i)
+        graph.replay()
+        want, wl = b.run()
+        _sync_ok()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert torch.all(out[1] == 0) and torch.all(lse[1] == -float("inf"))
+        for x, y in zip(a.state(), b.state()):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_operators_on_a_given_stream(raw):
+    """stream= as a torch stream and as a handle, another than the current one."""
+    a, b = _Step(60), _Step(60)
+    a.set(3)
+    b.set(3)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    s = st.cuda_stream if raw else st
+    out, lse = a.run(stream=s)
+    lens = q4.kv_evict_int8_paged(a.cache, a.mass, a.table, a.lens, 32, recent=4, stream=s)
+    k, v = q4.kv_gather_int8_paged(a.cache, a.slots, stream=s)
+    torch.cuda.current_stream().wait_stream(st)
+    want, wl = b.run()
+    wlens = q4.kv_evict_int8_paged(b.cache, b.mass, b.table, b.lens, 32, recent=4)
+    wk, wv = q4.kv_gather_int8_paged(b.cache, b.slots)
+    _sync_ok()
+    live = [0, 2]  # the padding row's keys and values are not written
+    for x, y in ((out, want), (lse, wl), (lens, wlens), (k[live], wk[live]), (v[live], wv[live])):
+        assert torch.equal(x, y)
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)
