@@ -73,7 +73,7 @@ constexpr float kKvLazy = 8.0f;
 
 __device__ __forceinline__ uint4 kv_ldg16(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
 
         const int32_t* trow = a.batch.table + static_cast<int64_t>(w.b) * a.batch.width;
         auto entry_of = [&](int j0) -> int32_t {
-            return P16 && j0 < seq.len ? __ldg(trow + page_index(j0)) : 0;
+            return P16 && j0 < seq.len ? kv_ld(trow + page_index(j0)) : 0;
         };
         // Element offsets of a token's row (of its scale; times d, of its codes) in the pools.
         struct Place {
@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
 #pragma unroll 1
                     for (int x = 0; x < Ring::copies; ++x) {
                         const int r = crow + x * Ring::rows, j = j0 + min(r, last);
-                        b = place(j, __ldg(trow + page_index(j)));
+                        b = place(j, kv_ld(trow + page_index(j)));
                         kv_cp16(st + Ring::k_at(r, cp), c.kc + b.kc + ccol);
                         if constexpr (!MASS) kv_cp16(st + Ring::half + Ring::v_at(r, cp), c.vc + b.vc + ccol);
                     }
-                    b = place(j0 + rs, __ldg(trow + page_index(j0 + rs)));
+                    b = place(j0 + rs, kv_ld(trow + page_index(j0 + rs)));
                 }
             }
             kv_cp_commit();
@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
             sc = 0;
             if constexpr (MASS) {
                 sc_mass = b.vs;
-                if (on && lane < 16) sc = __ldg(c.ks + b.ks);
+                if (on && lane < 16) sc = kv_ld(c.ks + b.ks);
             } else {
-                if (on) sc = __ldg(lane < 16 ? c.ks + b.ks : c.vs + b.vs);
+                if (on) sc = kv_ld(lane < 16 ? c.ks + b.ks : c.vs + b.vs);
             }
             if (i + 1 < nseg) entry_next = entry_of(j0 + kKvTile);
             put_sc = put;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = row0 + n * 8 + 2 * t + e, tok = r / a.geom.group;
-                    ls[n][e] = r < rows ? 1.44269504f * __ldg(a.lse + (seq.first + tok) * a.q_heads +
+                    ls[n][e] = r < rows ? 1.44269504f * kv_ld(a.lse + (seq.first + tok) * a.q_heads +
                                                               w.h * a.geom.group + r - tok * a.geom.group)
                                         : 0.f;
                 }

@@ -806,8 +806,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                                 kv_row(pc, w.h, j + 32 * e - page_index(j + 32 * e) * pc.ps);
                             ko = page * pc.kc_page + row * pc.d;
                             vo = page * pc.vc_page + row * pc.d;
-                            ks[e] = __ldg(pc.ks + page * pc.ks_page + row);
-                            vs[e] = __ldg(pc.vs + page * pc.vs_page + row);
+                            ks[e] = kv_ld(pc.ks + page * pc.ks_page + row);
+                            vs[e] = kv_ld(pc.vs + page * pc.vs_page + row);
                         }
                         sts64(rows + 256u * e, static_cast<uint64_t>(ko));
                         sts64(rows + 1024u + 256u * e, static_cast<uint64_t>(vo));

@@ -26,7 +26,7 @@ struct KvEvict {
 };
 
 __device__ __forceinline__ int kv_evict_len(const KvEvict& a, int b) {
-    int len = __ldg(a.batch.lens + b);
+    int len = kv_ld(a.batch.lens + b);
     if (len < 0 || len > a.batch.cap) {
         atomicOr(a.status, kStatusBadIndex);
         len = min(max(len, 0), a.batch.cap);
@@ -58,8 +58,8 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
 // equal to it, each CTA behind what the ones before it wrote.  Bound by
 // latency: 8 heads of 32,768 tokens took 100 us in 8 CTAs, and each digit
 // 5.5 us when one warp read the 8 CTAs' counts one after another; now 12 us in
-// 64 CTAs.  A thread takes four
-// consecutive tokens at a time (one 16-byte load where vec allows).
+// 64 CTAs.  A thread takes four consecutive tokens at a time (one 16-byte load
+// where vec allows).
 __global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __grid_constant__ KvEvict a, int C,
                                                                     int vec) {
     __shared__ uint32_t hist[4][256];
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __gri
         if (j >= j_end) return;
         if (vec) {
             const int e = shift >= 0 ? j >> shift : j / c.ps;
-            const int64_t page = kv_page(c, __ldg(trow + e), a.status);
-            const float4 m = __ldg(reinterpret_cast<const float4*>(mass + page * a.mass_page + (j - e * c.ps)));
+            const int64_t page = kv_page(c, kv_ld(trow + e), a.status);
+            const float4 m = kv_ld(reinterpret_cast<const float4*>(mass + page * a.mass_page + (j - e * c.ps)));
             k[0] = kv_mass_key(m.x);
             k[1] = kv_mass_key(m.y);
             k[2] = kv_mass_key(m.z);
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __gri
             for (int i = 0; i < 4; ++i) {
                 if (j + i >= j_end) break;
                 const int e = shift >= 0 ? (j + i) >> shift : (j + i) / c.ps;
-                const int64_t page = kv_page(c, __ldg(trow + e), a.status);
-                k[i] = kv_mass_key(__ldg(mass + page * a.mass_page + (j + i - e * c.ps)));
+                const int64_t page = kv_page(c, kv_ld(trow + e), a.status);
+                k[i] = kv_mass_key(kv_ld(mass + page * a.mass_page + (j + i - e * c.ps)));
             }
         }
     };
@@ -285,18 +285,17 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_select_kernel(const __gri
 // Source token of the i-th kept one.
 __device__ __forceinline__ int kv_evict_src(const KvEvict& a, int b, int h, int i, int len) {
     return len <= a.budget ? i
-                           : __ldg(a.src + (static_cast<int64_t>(b) * a.pool.heads + h) * a.budget + i);
+                           : kv_ld(a.src + (static_cast<int64_t>(b) * a.pool.heads + h) * a.budget + i);
 }
 // Its page among the destination's, or -1: what has no page is not moved.
 __device__ __forceinline__ int64_t kv_evict_dst_page(const KvEvict& a, int b, int i) {
-    const int32_t e = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_width + i / a.pool.ps);
+    const int32_t e = kv_ld(a.dst_table + static_cast<int64_t>(b) * a.dst_width + i / a.pool.ps);
     return kv_valid_page(a.pool, e, a.status) ? e : -1;
 }
 
 // Destination pages apart from the source pages: every kept row on its own (16
-// sequences of 1023 kept rows and 8 heads: 12 us).  A
-// team of TS lanes moves a row of K and of V (16 bytes a lane), its scales and
-// its mass.
+// sequences of 1023 kept rows and 8 heads: 12 us).  A team of TS lanes moves a
+// row of K and of V (16 bytes a lane), its scales and its mass.
 template <int TS>
 __global__ void __launch_bounds__(256) kv_evict_copy_kernel(const __grid_constant__ KvEvict a) {
     grid_launch_dependents();
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(256) kv_evict_inplace_kernel(const __grid_cons
         for (int i0 = 0; i0 < kept; i0 += 256) {
             const int i = i0 + threadIdx.x;
             int j = i;
-            if (i < kept) j = __ldg(a.src + static_cast<int64_t>(u) * a.budget + i);
+            if (i < kept) j = kv_ld(a.src + static_cast<int64_t>(u) * a.budget + i);
             const int64_t dp = i < kept && j > i ? kv_evict_dst_page(a, b, i) : -1;
             const bool move = dp >= 0;
             int64_t sp = 0, sr = 0, dr = 0;

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
                     kf[u * 4 + i][e + 2] = q8_pair<BF16>(xw[i], 0x4342u);
                 }
             }
-            sk[e] = in ? cache_value<BF16>(__ldg(c.ks + page[e] * c.ks_page + row[e])) * a.scale_log2 : 0.f;
+            sk[e] = in ? cache_value<BF16>(kv_ld(c.ks + page[e] * c.ks_page + row[e])) * a.scale_log2 : 0.f;
         }
         // rows that see any of the 16 tokens: those of new tokens with at >= j0 and,
         // under a window, at - window < j0 + 15
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
 #pragma unroll
             for (int s = 0; s < DP / 16; ++s) {
                 const int e = (s >> 2) * 64 + t * 16 + (s & 3) * 4;
-                const uint2 qf = r < r_hi && e < d ? __ldg(reinterpret_cast<const uint2*>(qp + e))
+                const uint2 qf = r < r_hi && e < d ? kv_ld(reinterpret_cast<const uint2*>(qp + e))
                                                    : make_uint2(0u, 0u);
                 mma_16816<BF16>(x, kf[s], qf.x, qf.y);
             }
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
                 const int rr = r0 + 2 * t + e;
                 if (rr < r_hi) {
                     const int tk = rr / a.geom.group;
-                    const float ls = __ldg(a.lse + (seq.first + tk) * a.q_heads + h * a.geom.group +
+                    const float ls = kv_ld(a.lse + (seq.first + tk) * a.q_heads + h * a.geom.group +
                                            rr - tk * a.geom.group) * 1.44269504f;
                     const int last = seq.len - seq.n + tk;
 #pragma unroll

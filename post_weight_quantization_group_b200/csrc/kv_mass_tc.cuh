@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
                 live = kv_valid_page(a.pool, entry, a.status);  // else there is nothing to add to
                 const int64_t page = live ? entry : 0;
                 const int64_t row = kv_row(a.pool, g.h, j - e * a.pool.ps);
-                sk = cache_value<BF16>(__ldg(a.pool.ks + page * a.pool.ks_page + row)) * a.scale_log2;
+                sk = cache_value<BF16>(kv_ld(a.pool.ks + page * a.pool.ks_page + row)) * a.scale_log2;
                 place = page * a.mass_page + row;
             }
             const uint64_t sk2 = f2_pack(sk, sk);
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_mass_tc_kernel(const __grid
                     int at = -1;
                     if (row < r_hi) {
                         const int tok = row / a.group;
-                        nl = -1.44269504f * __ldg(a.lse + (first + tok) * a.q_heads + h * a.group + row -
+                        nl = -1.44269504f * kv_ld(a.lse + (first + tok) * a.q_heads + h * a.group + row -
                                                   tok * a.group);
                         at = past + tok;
                     }

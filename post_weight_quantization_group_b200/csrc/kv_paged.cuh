@@ -15,6 +15,16 @@
 
 namespace q4dev {
 
+// A load of what another kernel of the stream may have written: a plain one.
+// These kernels begin while the one ahead of them still runs (programmatic
+// launch), so nothing they read is constant for as long as they run, which is
+// what the read-only path asks for: a line of it that an earlier kernel left in
+// the SM could be stale.
+template <typename T>
+__device__ __forceinline__ T kv_ld(const T* p) {
+    return *p;
+}
+
 struct KvPool {
     int8_t *kc, *vc;
     uint16_t *ks, *vs;
@@ -47,11 +57,11 @@ struct KvSeq {
 // device arrays say more than the buffers hold.
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int i, unsigned* status) {
     KvSeq s;
-    int len = __ldg(b.lens + i);
+    int len = kv_ld(b.lens + i);
     int64_t lo, hi;
     if (b.cu) {
-        lo = __ldg(b.cu + i);
-        hi = __ldg(b.cu + i + 1);
+        lo = kv_ld(b.cu + i);
+        hi = kv_ld(b.cu + i + 1);
     } else {
         lo = i;
         hi = i + 1;
@@ -71,7 +81,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int i, unsigned* statu
 // Table entry e of sequence i, and the page it names, brought into [0, pages)
 // likewise.  Two steps, so that a kernel can load an entry ahead of its use.
 __device__ __forceinline__ int32_t kv_entry(const KvBatch& b, int i, int e) {
-    return __ldg(b.table + static_cast<int64_t>(i) * b.width + e);
+    return kv_ld(b.table + static_cast<int64_t>(i) * b.width + e);
 }
 __device__ __forceinline__ bool kv_valid_page(const KvPool& c, int32_t entry, unsigned* status) {
     if (entry >= 0 && entry < c.pages) return true;
@@ -151,8 +161,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
     const int h_end = min(h_beg + a.heads_per_cta, a.q_heads + 2 * c.heads);
     const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;
     uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (on && a.q_norm) wq = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + sub);
-    if (on && a.k_norm) wk = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + sub);
+    if (on && a.q_norm) wq = kv_ld(reinterpret_cast<const uint4*>(a.q_norm) + sub);
+    if (on && a.k_norm) wk = kv_ld(reinterpret_cast<const uint4*>(a.k_norm) + sub);
     const float inv_d = 1.f / static_cast<float>(d);
 
     auto load = [&](int64_t tok, int h) -> uint4 {
@@ -168,8 +178,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
     };
     auto angles = [&](int64_t tok, float2* to) {
         for (int i = threadIdx.x; i < half; i += 256) {
-            double t = static_cast<double>(__ldg(a.positions + tok)) *
-                       static_cast<double>(__ldg(a.inv_freq + i)) * 0.15915494309189533577;
+            double t = static_cast<double>(kv_ld(a.positions + tok)) *
+                       static_cast<double>(kv_ld(a.inv_freq + i)) * 0.15915494309189533577;
             t -= rint(t);
             float s, co;
             sincospif(static_cast<float>(2.0 * t), &s, &co);
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
     if (tok >= a.tokens) return;
     uint4 nxt = load(tok, h_beg + team);
     angles(tok, cs[0]);
-    int64_t slot = __ldg(a.slots + tok);
+    int64_t slot = kv_ld(a.slots + tok);
     __syncthreads();
     for (int buf = 0; tok < a.tokens; buf ^= 1) {
         const int64_t next = tok + gridDim.x;
@@ -191,7 +201,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
         const bool write = slot >= 0 && page < c.pages;
         if (slot >= 0 && !write && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);
         if (next < a.tokens) {
-            slot = __ldg(a.slots + next);
+            slot = kv_ld(a.slots + next);
             angles(next, cs[buf ^ 1]);
         }
         // This lane's part of the rotation: v' = v f.x + partner f.y, element by element, or
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(256)
          it += static_cast<int64_t>(gridDim.x) * TEAMS) {
         const int64_t tok = it / (2 * c.heads);
         const int hh = static_cast<int>(it - tok * (2 * c.heads));
-        const int64_t slot = __ldg(slots + tok);
+        const int64_t slot = kv_ld(slots + tok);
         const int64_t page = slot / c.ps;
         if (slot < 0 || sub * 8 >= c.d) continue;
         if (page >= c.pages) {

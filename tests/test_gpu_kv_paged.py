@@ -788,3 +788,33 @@ def test_operators_on_a_given_stream(raw):
         assert torch.equal(x, y)
     for x, y in zip(a.state(), b.state()):
         assert torch.equal(x, y)
+
+
+def test_calls_right_behind_one_another():
+    """Evictions, attention over the lengths that they return, mass and appends
+    without a pause between them, in rounds over three caches,
+    each call's data written by the one before it, against the same calls with
+    a wait after each."""
+    def steps(wait):
+        out = []
+
+        def ran(*x):
+            if wait:
+                torch.cuda.synchronize()
+            out.extend(x)
+        st = [_Step(70 + i) for i in range(3)]
+        for i, s in enumerate(st):
+            s.set(2 * i)
+        torch.cuda.synchronize()
+        for r in range(4):
+            for s in st:
+                s.lens = q4.kv_evict_int8_paged(s.cache, s.mass, s.table, s.lens, 120 - 20 * r, recent=4)
+                ran(s.lens)
+            for s in st:
+                ran(*s.run())
+        ran(*(x for s in st for x in s.state()))
+        torch.cuda.synchronize()
+        return out
+    for x, y in zip(steps(False), steps(True)):
+        assert torch.equal(x, y)
+    _sync_ok()
