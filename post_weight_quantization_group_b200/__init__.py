@@ -747,6 +747,11 @@ def _int32(t: torch.Tensor | None, what: str, shape):
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
 
 
+def _own_workspace(t: torch.Tensor | None):
+    if t is not None and not t.is_contiguous():  # its bytes are counted from its elements
+        raise ValueError("workspace must be contiguous")
+
+
 def _kv_batch(block_table, seq_lens, cu_new, tokens: int, max_new: int) -> _CKVBatch:
     if block_table.dim() != 2:
         raise ValueError("block_table must be [seqs, width]")
@@ -847,6 +852,7 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     qs = _head_rows(q, "q", None, d, dt)
     hq = q.shape[1]
     batch = _kv_batch(block_table, seq_lens, cu_new, tokens, max_new)
+    _own_workspace(workspace)
     _same_device(cache.k_codes, q, block_table, seq_lens, cu_new, out, lse, workspace)
     with _Call(q.device, stream) as call:
         if out is None:
@@ -917,6 +923,7 @@ def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: tor
             raise ValueError("dst_table must be [seqs, width]")
         _int32(dst_table, "dst_table", (seqs, dst_table.shape[1]))
     _int32(new_lens, "new_lens", (seqs,))
+    _own_workspace(workspace)
     _same_device(cache.k_codes, mass, block_table, seq_lens, dst_table, new_lens, workspace)
     with _Call(seq_lens.device, stream) as call:
         if new_lens is None:

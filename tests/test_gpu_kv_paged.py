@@ -818,3 +818,19 @@ def test_calls_right_behind_one_another():
     for x, y in zip(steps(False), steps(True)):
         assert torch.equal(x, y)
     _sync_ok()
+
+
+def test_refused_workspaces():
+    """A workspace that is not one run of bytes, is too small, or lies on the host."""
+    s = _Step(80)
+    s.set(1)
+    q = s.qkv[:, :s.hq].contiguous()
+    for ws, err in ((torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 26), ValueError),
+                    (torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")[::2], ValueError),
+                    (torch.zeros(64, dtype=torch.uint8, device="cuda"), q4.Q4Error),
+                    (torch.zeros(1 << 26, dtype=torch.uint8), ValueError)):
+        with pytest.raises(err):
+            q4.kv_attention_int8_paged(s.cache, q, s.table, s.lens, workspace=ws)
+        with pytest.raises(err):
+            q4.kv_evict_int8_paged(s.cache, s.mass, s.table, s.lens, 32, workspace=ws)
+    _sync_ok()
