@@ -141,11 +141,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 //   pos * inv_freq in turns, reduced in fp64 (53 bits keep a position of 2^31
 //   within 2e-7 of a turn), then sine and cosine of the remainder in fp32.
 // K is quantized from its fp32 rotated value: a rounding to the cache type in
-// between would add an error of its own.  Bound by memory for long prompts
-// (every element is read and written once) with the instruction rate close
-// behind, so a warp whose heads are all queries has a path of its own, without
-// the quantization and without branches (8191 tokens of 64/8 heads of 128:
-// 98 us, 3.1 TB/s; with branches and one path 130).  PAIRS: interleaved rotation.
+// between would add an error of its own.  Every element is read and written
+// once; bound by the instruction rate (0.71 of the issue slots), so a warp
+// whose heads are all queries has a path of its own, without the quantization
+// and without branches (8191 tokens of 64/8 heads of 128: 98 us, 3.1 TB/s; with
+// branches and one path 130; three heads under way instead of one 98; the
+// weights multiplied into the angles and packed fp32 pairs 103, as they cost
+// each token more than its five heads a warp save).  PAIRS: interleaved rotation.
 template <bool BF16, int TS, bool PAIRS>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppend a) {
     constexpr int TEAMS = 256 / TS;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
             angles(next, cs[buf ^ 1]);
         }
         // This lane's part of the rotation: v' = v f.x + partner f.y, element by element, or
-        // pair by pair; (1, 0) where nothing turns.
+        // pair by pair.  Elements behind rot_dim keep what they hold, an infinity too.
         float2 f[PAIRS ? 4 : 8];
         const bool lo = sub < hl;
         const int peer = PAIRS ? 0 : lane0 + (lo ? sub + hl : sub < 2 * hl ? sub - hl : sub);
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = v[2 * i], y = v[2 * i + 1];
+                    if (sub * 4 + i >= half) continue;
                     v[2 * i] = x * f[i].x - y * f[i].y;
                     v[2 * i + 1] = y * f[i].x + x * f[i].y;
                 }
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float y = __shfl_sync(0xFFFFFFFFu, v[i], peer);
-                    v[i] = fmaf(v[i], f[i].x, y * f[i].y);
+                    if (sub < 2 * hl) v[i] = fmaf(v[i], f[i].x, y * f[i].y);
                 }
             }
         };
@@ -313,9 +316,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
 // rounding of an exact product.  A team per (token, K or V, head).
 template <bool BF16, int TS>
 __global__ void __launch_bounds__(256)
-    kv_gather_kernel(const __grid_constant__ KvPool c, const int64_t* __restrict__ slots,
-                     int64_t tokens, uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                     unsigned* __restrict__ status) {
+    kv_gather_kernel(const __grid_constant__ KvPool c, const int64_t* slots, int64_t tokens,
+                     uint16_t* k_out, uint16_t* v_out, unsigned* status) {
     constexpr int TEAMS = 256 / TS;
     grid_launch_dependents();
     grid_dependency_wait();

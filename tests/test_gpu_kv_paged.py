@@ -834,3 +834,23 @@ def test_refused_workspaces():
         with pytest.raises(err):
             q4.kv_evict_int8_paged(s.cache, s.mass, s.table, s.lens, 32, workspace=ws)
     _sync_ok()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq", [1, 40])
+def test_append_infinities_behind_the_rotation(hq, interleaved):
+    """What is not rotated comes out as it went in, infinities among it, and
+    they reach no other element."""
+    tokens, d, rot, dt = 3, 64, 32, BF
+    g = _gen(90)
+    qkv = torch.randn(tokens, hq + 2, d, generator=g, device="cuda").to(dt)
+    qkv[:, :hq, rot + 5] = float("inf")
+    qkv[:, :hq, d - 1] = -float("inf")
+    cache = _pool(2, 1, 16, d, dt, 91)
+    pos = _cuda32([3, 1000, 77])
+    inv = (10000.0 ** (-torch.arange(0, rot, 2, device="cuda").double() / rot)).float()
+    got = q4.kv_append_int8_paged(cache, qkv[:, :hq], qkv[:, hq:hq + 1], qkv[:, hq + 1:],
+                                  torch.arange(tokens, device="cuda"), pos, inv, interleaved=interleaved)
+    _sync_ok()
+    assert torch.equal(got[..., rot:], qkv[:, :hq, rot:])
+    assert torch.all(torch.isfinite(got[..., :rot]))
