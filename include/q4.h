@@ -607,8 +607,10 @@ Q4_API q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t*
  * k_j, v_j the dequantized rows (q * s, not rounded).  A row that sees nothing
  * gives zeros and lse = -inf.  q_heads is a multiple of the cache's heads:
  * query head h reads KV head h / (q_heads / heads).  The softmax is in fp32
- * with one rounding of the weights to fp16 (2^-11) before the product with V.
- * V scales below 2^-100 count as 2^-100.  A masked token's row does not reach
+ * with one rounding of the weights before the product with V: of weight times
+ * V scale to fp16 (2^-11), or to 2^-32 of the row's largest where that is more.
+ * V scales below 2^-80 count as 2^-80.  Sums are in fp32: one over n tokens may lose
+ * n * 2^-23 of itself.  A masked token's row does not reach
  * the output whatever its scales hold; a visible NaN does.
  *   q          [tokens, q_heads, head_dim] in the cache type, rows q_stride apart
  *   out        the same shape, rows out_stride apart; must not overlap q

@@ -5,12 +5,16 @@
 //   out_r = sum_j 2^(S log2e - m) sv_j vq_j / sum_j 2^(S log2e - m).
 //
 // The V scale goes into the exponent: with x = S log2e + log2 sv and
-// p' = 2^(x - m'), m' the running maximum of x, the numerator is
-// sum p' vq and the denominator sum p' / sv.  p' has its maximum near 1 whatever
+// p' = 2^(x - m'), m' a whole number below the running maximum of x, the numerator is
+// sum p' vq and the denominator sum p' / sv.  p' has its maximum at 2^7 to 2^15 whatever
 // the V scales are, so it can be rounded to fp16 (2^-11, as fine as the
 // codes' own exact fp16 form allows for the product) without leaving fp16's
-// range; the denominator adds the unrounded fp32 p'.  V scales below 2^-100
-// are taken as 2^-100 (an absolute error below 2^-93).
+// range above, and down to 2^-21 of the row's largest p' without leaving its normals;
+// below that it is off by up to 2^-32 of the largest (with the maximum near 1 that would be
+// 2^-25, and 10^5 tokens far below one other lost 1% of the output).  The
+// denominator adds the unrounded fp32 p'.  V scales below 2^-80 are taken as 2^-80 (an
+// absolute error below 2^-73): the denominator of 2^30 tokens, at most 2^(15 + 80 + 30),
+// stays in fp32.
 //
 // Bound by the cache bytes read once from HBM.  A warp works alone on blocks
 // of 16 tokens: cp.async brings a block's codes into its own ring of shared
@@ -67,9 +71,14 @@ struct KvAttn {
 constexpr int kKvWarps = 8;
 constexpr int kKvTile = 16 * kKvWarps;  // tokens of a tile
 constexpr float kKvNone = -1e30f;       // the maximum of nothing: finite, so that m - m' is not NaN
-// A warp rescales only when a score passes its maximum by more than this
-// (log2): p' stays below 2^8, inside fp16, and most blocks skip the rescale.
-constexpr float kKvLazy = 8.0f;
+// A warp takes another m' only when an x passes it by more than kKvTop: p' stays
+// below 2^15, inside fp16, and most blocks skip the rescale.  The new m' lies kKvBelow to
+// kKvBelow + 1 under that x, so a row's largest p' is 2^7 or more.  It is whole, so
+// the factors of a rescale are powers of two and exact.
+constexpr float kKvTop = 15.0f, kKvBelow = 7.0f;
+__device__ __forceinline__ float kv_new_max(float m, float x) {
+    return x > m + kKvTop ? floorf(x) - kKvBelow : m;
+}
 
 __device__ __forceinline__ uint4 kv_ldg16(const void* p) {
     uint4 v;
@@ -108,7 +117,7 @@ struct KvVScale {
 };
 __device__ __forceinline__ KvVScale kv_vscale(float sv) {
     KvVScale r;
-    const float c = fmaxf(sv, 7.888609e-31f);  // 2^-100; a NaN becomes 2^-100 here ...
+    const float c = fmaxf(sv, 0x1p-80f);  // a NaN becomes 2^-80 here ...
     r.lg = sv == sv ? __log2f(c) : sv;         // ... and stays in the exponent, where masks drop it
     // within 1 ulp; c is normal and, as 1/127 of a finite value, below 2^121
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(c));
@@ -464,8 +473,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         if (!see) x[n][e] = -INFINITY;
                     }
                 }
-                grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kKvLazy ||
-                        fmaxf(x[n][1], x[n][3]) > m[n][1] + kKvLazy;
+                grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kKvTop ||
+                        fmaxf(x[n][1], x[n][3]) > m[n][1] + kKvTop;
             }
             if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
                         for (int off = 4; off < 32; off <<= 1)
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
                         // a row of its own: what other rows of the warp do leaves it alone
-                        mx = mx > m[n][e] + kKvLazy ? mx : m[n][e];
+                        mx = kv_new_max(m[n][e], mx);
                         f[e] = kv_exp2(m[n][e] - mx);
                         m[n][e] = mx;
                         l[n][e] *= f[e];

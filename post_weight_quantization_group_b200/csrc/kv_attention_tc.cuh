@@ -8,7 +8,7 @@
 // thread owns one row of it (no shuffles), writes p' as fp16 over the same
 // columns, and O += P V reads it there as the A operand.  While one half is
 // in its softmax the tensor pipe works on the other.  O stays in tensor
-// memory; it is rescaled only when a row's maximum grows by more than kKvLazy.
+// memory; it is rescaled only when a row's x passes its m' by more than kKvTop.
 //
 // Measured (B200): 1024 new tokens over 32,768, 64 query heads over 8 of 128,
 // 1.66 ms = 657 TFLOP/s; bound by the latency of the softmax warps' instructions
@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                     scx = sbase + G::off_one + (lane & 3) * 8u;
                 }
                 // One pass, 32 columns at a time, the next ones' S on its way: x = S sk + lg,
-                // p' = 2^(x - m) with the maximum known so far, their sum with 1 / sv into l. The
+                // p' = 2^(x - m) with the m' known so far, their sum with 1 / sv into l. The
                 // packed p' of columns 16 q .. go over columns 8 q .. of S, which have been read.
-                // A chunk whose maximum is more than kKvLazy above m (rare after a segment's
-                // first tile) raises m first and rescales what has been added with the old one:
-                // l, O and this tile's earlier weights (a second rounding to fp16 for those).
+                // Columns whose maximum is more than kKvTop above m (rare after a segment's
+                // first tile) raise m first and rescale what has been added with the old one by a
+                // power of two: l, O and this tile's earlier weights (a second rounding for those
+                // that it takes below fp16's normals).
                 uint64_t lx[4], neg_m[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) f2_unpack(x[4 * y + k], u[y], t[y]);
                         mx[k] = fmaxf(f_max3(f_max3(u[0], t[0], u[1]), t[1], u[2]), f_max3(t[2], u[3], t[3]));
-                        grow |= mx[k] > m[k] + kKvLazy;
+                        grow |= mx[k] > m[k] + kKvTop;
                     }
                     if (__any_sync(0xFFFFFFFFu, grow)) {
                         float f[4];
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
                             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
                             // each row of its own: what the warp's other rows do leaves it alone
-                            const float mn = mx[k] > m[k] + kKvLazy ? mx[k] : m[k];
+                            const float mn = kv_new_max(m[k], mx[k]);
                             f[k] = kv_exp2(m[k] - mn);
                             m[k] = mn;
                             lx[k] = f2_fma(lx[k], f2_pack(f[k], f[k]), 0ull);
