@@ -591,6 +591,23 @@ Q4_API q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q,
                                       void* q_out, int64_t q_out_stride, q4_stream stream);
 
 /*
+ * The same call for a cache whose attention mass is kept: the slots that get a
+ * key and value have their mass set to zero, since what a slot holds there is its last
+ * token's (an eviction leaves it behind the kept rows, and so does a page that another
+ * sequence gives back).  Who appends by kv_append_int8_paged clears it themselves.
+ *   mass  fp32 [pages, heads, page_size], pages mass_stride elements apart, or NULL
+ */
+Q4_API q4_status kv_append_mass_int8_paged(const kv_paged_int8* cache, const void* q,
+                                           int64_t q_stride, int32_t q_heads, const void* k,
+                                           int64_t k_stride, const void* v, int64_t v_stride,
+                                           int64_t tokens, const int64_t* slots,
+                                           const int32_t* positions, const float* inv_freq,
+                                           int32_t rot_dim, int32_t interleaved,
+                                           const void* q_norm, const void* k_norm, float eps,
+                                           void* q_out, int64_t q_out_stride, float* mass,
+                                           int64_t mass_stride, q4_stream stream);
+
+/*
  * Cached rows by slot: k_out[t, h] = cache_type(q * s) of the key in slots[t],
  * v_out likewise; both dense [tokens, heads, head_dim], 16-byte aligned.  Rows
  * of negative slots are left as they are.
@@ -640,6 +657,8 @@ Q4_API q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void*
  *         same queries, scale and window
  *   mass  fp32 [pages, heads, page_size], pages mass_stride elements apart
  * A page that several sequences share gets the sum of theirs (in any order).
+ * A slot's mass has to be zero when a token is written there: see
+ * kv_append_mass_int8_paged.
  */
 Q4_API q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const void* q,
                                               int64_t q_stride, int32_t q_heads, const float* lse,
@@ -651,7 +670,8 @@ Q4_API q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const 
  * `recent` and, of the others, those of the largest mass (equal masses: the
  * lower index; a NaN is below all), `budget` in all -- or everything, where it has no more --
  * and the kept rows of K, V, scales and mass move, in their order, to tokens
- * 0, 1, ... of the destination pages.  What lies behind them stays as it is.
+ * 0, 1, ... of the destination pages.  What lies behind them stays as it is, its
+ * mass too: the tokens that come to lie there are appended with kv_append_mass_int8_paged.
  *   batch     block_table, seq_lens, table_width, seqs (the rest is not used)
  *   budget    >= 1;  recent, sinks >= 0, recent + sinks <= budget
  *   dst_table [seqs, dst_width] pages that get the kept tokens, none of them a

@@ -47,7 +47,7 @@ ABI_SYMBOLS = (
     "q8_gemv", "kv_quantize_int8", "kv_dequant_int8", "kv_quantize_int4", "kv_dequant_int4",
     "mxfp4_quantize", "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "q4_gemv_grouped",
     "fp4_gemm_workspace_bytes", "fp4_gemm", "bf16_ref_workspace_bytes",
-    "kv_append_int8_paged", "kv_gather_int8_paged", "kv_attention_workspace_bytes",
+    "kv_append_int8_paged", "kv_append_mass_int8_paged", "kv_gather_int8_paged", "kv_attention_workspace_bytes",
     "kv_attention_int8_paged", "kv_attention_mass_int8_paged", "kv_evict_workspace_bytes",
     "kv_evict_int8_paged",
 )
@@ -158,6 +158,7 @@ def load_library(path: str = LIB_PATH):
     KV, KB, F, Z = ctypes.POINTER(_CKVPaged), ctypes.POINTER(_CKVBatch), ctypes.c_float, ctypes.c_size_t
     lib.kv_append_int8_paged.argtypes = [KV, P, I64, I32, P, I64, P, I64, I64, P, P, P, I32, I32, P,
                                          P, F, P, I64, P]
+    lib.kv_append_mass_int8_paged.argtypes = [*lib.kv_append_int8_paged.argtypes[:-1], P, I64, P]
     lib.kv_gather_int8_paged.argtypes = [KV, P, I64, P, P, P]
     lib.kv_attention_workspace_bytes.argtypes = [I32, I32, I32, I64]
     lib.kv_attention_workspace_bytes.restype = Z
@@ -173,7 +174,7 @@ def load_library(path: str = LIB_PATH):
               "q8_quantize_per_channel", "q8_dequant", "q8_gemv", "kv_quantize_int8",
               "kv_dequant_int8", "kv_quantize_int4", "kv_dequant_int4", "mxfp4_quantize",
               "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "fp4_gemm", "kv_append_int8_paged",
-              "kv_gather_int8_paged", "kv_attention_int8_paged", "kv_attention_mass_int8_paged",
+              "kv_append_mass_int8_paged", "kv_gather_int8_paged", "kv_attention_int8_paged", "kv_attention_mass_int8_paged",
               "kv_evict_int8_paged"):
         getattr(lib, f).restype = S
     lib.q4_status_string.argtypes = [S]
@@ -768,13 +769,16 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
                          inv_freq: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
                          k_norm: torch.Tensor | None = None, eps: float = 1e-6,
                          interleaved: bool = False, q_out: torch.Tensor | None = None,
-                         stream=None) -> torch.Tensor | None:
+                         stream=None, mass: torch.Tensor | None = None) -> torch.Tensor | None:
     """The new tokens of a layer into its cache: query / key RMS norm (where a
     weight is given), rotation by position (where inv_freq [rot_dim / 2] is),
     INT8 quantization of k and v into slots (int64 [tokens], page * page_size +
     offset, negative: padding).  q [tokens, q_heads, head_dim], k and v
-    [tokens, heads, head_dim]: slices of a fused projection will do.  Returns
-    the queries (q_out, which may be q; None without q)."""
+    [tokens, heads, head_dim]: slices of a fused projection will do.  mass: the
+    attention mass of the pool (fp32 [pages, heads, page_size]), where one is kept;
+    the written slots' is set to zero, so that a new token does not start with
+    its slot's last one's.  Returns the queries (q_out, which may be q; None
+    without q)."""
     lib = load_library()
     cs = cache.c_struct()
     dt, d = cache.dtype, cs.head_dim
@@ -795,19 +799,21 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
     for w in (q_norm, k_norm):
         if w is not None and (w.dtype != dt or w.shape != (d,) or not w.is_contiguous()):
             raise ValueError("norm weights must be [head_dim] in the cache type")
-    _same_device(cache.k_codes, q, k, v, slots, positions, inv_freq, q_norm, k_norm, q_out)
+    ms = _mass_stride(cache, mass) if mass is not None else 0
+    _same_device(cache.k_codes, q, k, v, slots, positions, inv_freq, q_norm, k_norm, q_out, mass)
     with _Call(k.device, stream) as call:
         if q is not None and q_out is None:
             q_out = _empty_as(q)
         os_ = _head_rows(q_out, "q_out", q.shape[1], d, dt, tokens) if q is not None else 0
-        st = lib.kv_append_int8_paged(
+        st = lib.kv_append_mass_int8_paged(
             ctypes.byref(cs), q.data_ptr() if q is not None else None, qs,
             q.shape[1] if q is not None else 0, k.data_ptr(), ks, v.data_ptr(), vs, tokens,
             slots.data_ptr(), positions.data_ptr() if positions is not None else None,
             inv_freq.data_ptr() if inv_freq is not None else None, rot, int(interleaved),
             q_norm.data_ptr() if q_norm is not None else None,
             k_norm.data_ptr() if k_norm is not None else None, eps,
-            q_out.data_ptr() if q is not None else None, os_, call.handle)
+            q_out.data_ptr() if q is not None else None, os_,
+            mass.data_ptr() if mass is not None else None, ms, call.handle)
     _check(st, "kv_append_int8_paged")
     return q_out
 
@@ -880,7 +886,8 @@ def kv_attention_mass_int8_paged(cache: KVPagedInt8, q: torch.Tensor, lse: torch
                                  stream=None) -> torch.Tensor:
     """Adds to mass (fp32 [pages, heads, page_size]) the attention weight that
     each cached token received from these queries; lse as the attention call
-    with the same arguments returned it.  Returns mass."""
+    with the same arguments returned it.  A token's mass has to start at zero: append
+    with mass=.  Returns mass."""
     lib = load_library()
     cs = cache.c_struct()
     tokens, hq = q.shape[0], q.shape[1]
@@ -911,8 +918,9 @@ def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: tor
                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Cuts every sequence to ``budget`` tokens per KV head: the first
     ``sinks``, the last ``recent`` and the heaviest of the others by mass, moved
-    in order into the pages of dst_table (None: in place).  Returns the new
-    lengths (int32 [seqs])."""
+    in order into the pages of dst_table (None: in place).  What lies behind them
+    keeps its mass: append the tokens that come there with mass=.  Returns the
+    new lengths (int32 [seqs])."""
     lib = load_library()
     cs = cache.c_struct()
     ms = _mass_stride(cache, mass)

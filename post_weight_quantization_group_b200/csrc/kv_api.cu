@@ -240,6 +240,18 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
                                const int32_t* positions, const float* inv_freq, int32_t rot_dim,
                                int32_t interleaved, const void* q_norm, const void* k_norm,
                                float eps, void* q_out, int64_t q_out_stride, q4_stream stream) {
+    return kv_append_mass_int8_paged(cache, q, q_stride, q_heads, k, k_stride, v, v_stride, tokens, slots,
+                                     positions, inv_freq, rot_dim, interleaved, q_norm, k_norm, eps, q_out,
+                                     q_out_stride, nullptr, 0, stream);
+}
+
+q4_status kv_append_mass_int8_paged(const kv_paged_int8* cache, const void* q, int64_t q_stride,
+                                    int32_t q_heads, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, int64_t tokens, const int64_t* slots,
+                                    const int32_t* positions, const float* inv_freq, int32_t rot_dim,
+                                    int32_t interleaved, const void* q_norm, const void* k_norm,
+                                    float eps, void* q_out, int64_t q_out_stride, float* mass,
+                                    int64_t mass_stride, q4_stream stream) {
     q4_status s = check_pool(cache);
     if (s != Q4_OK) return s;
     if (tokens < 0 || q_heads < 0 || q_heads > (1 << 20)) return Q4_ERR_SHAPE;
@@ -247,6 +259,7 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
         return Q4_ERR_SHAPE;
     if (interleaved != 0 && interleaved != 1) return Q4_ERR_INVALID_ARG;
     if (!std::isfinite(eps) || eps < 0.f) return Q4_ERR_INVALID_ARG;
+    if (mass && mass_stride < static_cast<int64_t>(cache->heads) * cache->page_size) return Q4_ERR_SHAPE;
     if (tokens == 0) return Q4_OK;
     const int64_t d = cache->head_dim;
     if (!slots || (rot_dim > 0 && (!positions || !inv_freq))) return Q4_ERR_INVALID_ARG;
@@ -257,7 +270,7 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
         if ((s = check_rows(q_out, q_out_stride, q_heads * d)) != Q4_OK) return s;
     }
     if (!aligned(slots, 8) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
-        !aligned(q_norm, 16) || !aligned(k_norm, 16))
+        !aligned(q_norm, 16) || !aligned(k_norm, 16) || !aligned(mass, 4))
         return Q4_ERR_ALIGNMENT;
     KvAppend a{};
     a.pool = pool_of(cache);
@@ -274,6 +287,8 @@ q4_status kv_append_int8_paged(const kv_paged_int8* cache, const void* q, int64_
     a.slots = slots;
     a.positions = positions;
     a.inv_freq = inv_freq;
+    a.mass = mass;
+    a.mass_page = mass_stride;
     a.tokens = tokens;
     a.q_heads = q_heads;
     a.rot = rot_dim;

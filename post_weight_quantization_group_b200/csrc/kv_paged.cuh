@@ -104,6 +104,8 @@ struct KvAppend {
     const int64_t* slots;
     const int32_t* positions;
     const float* inv_freq;  // [rot / 2]
+    float* mass;            // [pages, heads, page_size], pages mass_page apart, or null
+    int64_t mass_page;
     int64_t tokens;
     int q_heads, rot, heads_per_cta;
     float eps;
@@ -305,7 +307,11 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
             const int64_t row = kv_row(c, h - a.q_heads - (is_v ? c.heads : 0), off);
             int8_t* codes = (is_v ? c.vc + page * c.vc_page : c.kc + page * c.kc_page) + row * d;
             *reinterpret_cast<uint2*>(codes + sub * 8) = packed;
-            if (sub == 0) (is_v ? c.vs + page * c.vs_page : c.ks + page * c.ks_page)[row] = sbits;
+            if (sub == 0) {
+                (is_v ? c.vs + page * c.vs_page : c.ks + page * c.ks_page)[row] = sbits;
+                // what the slot's last token received is not the new one's
+                if (a.mass && !is_v) a.mass[page * a.mass_page + row] = 0.f;
+            }
         }
         __syncthreads();  // the next token's angles are there, and this one's are done with
         tok = next;

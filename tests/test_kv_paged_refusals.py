@@ -1,0 +1,35 @@
+"""Refusals of the paged INT8 KV-cache calls on the host, before any CUDA call.
+No GPU needed; every call here is refused or has nothing to do."""
+import ctypes
+
+import pytest
+
+import post_weight_quantization_group_b200 as q4
+from post_weight_quantization_group_b200 import build as q4build
+from test_kv_paged_abi import A, POOL_FAULTS, _pool, _status
+
+
+@pytest.fixture(scope="module")
+def lib():
+    q4build.build()
+    return q4.load_library()
+
+
+def _append_mass(lib, pool=None, **kw):
+    a = dict(k=A, n=3, mass=A, ms=32)
+    a.update(kw)
+    return lib.kv_append_mass_int8_paged(ctypes.byref(pool or _pool()), A, 256, 4, a["k"], 128, A, 128, a["n"], A, A,
+                                         A, 64, 0, None, None, 1e-6, A, 256, a["mass"], a["ms"], None)
+
+
+@pytest.mark.parametrize("kw,status", POOL_FAULTS)
+def test_append_mass_pool_faults(lib, kw, status):
+    assert _append_mass(lib, _pool(**kw)) == _status(status)
+
+
+def test_append_mass_faults(lib):
+    assert _append_mass(lib, n=0) == q4.Q4_OK
+    assert _append_mass(lib, n=0, mass=None, ms=0) == q4.Q4_OK
+    assert _append_mass(lib, ms=31) == q4.Q4_ERR_SHAPE
+    assert _append_mass(lib, mass=A + 2) == q4.Q4_ERR_ALIGNMENT
+    assert _append_mass(lib, k=None) == q4.Q4_ERR_INVALID_ARG
