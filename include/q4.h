@@ -650,6 +650,18 @@ Q4_API q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void*
                                          size_t workspace_bytes, q4_stream stream);
 
 /*
+ * The same call for outputs that hold nothing yet: rows of q that no sequence
+ * names (a batch padded to a fixed number of rows) are filled instead of left.
+ *   fill  0 as above; 1: their rows of out become zeros; 2: of lse -inf; 3: both
+ */
+Q4_API q4_status kv_attention_fill_int8_paged(const kv_paged_int8* cache, const void* q,
+                                              int64_t q_stride, int32_t q_heads,
+                                              const kv_batch* batch, float scale, int64_t window,
+                                              void* out, int64_t out_stride, float* lse,
+                                              void* workspace, size_t workspace_bytes,
+                                              int32_t fill, q4_stream stream);
+
+/*
  * The attention weight the cached tokens received from these queries, added to
  * what earlier calls found: for every sequence, KV head h and token j
  *   mass[page, h, slot] += sum over the rows of h that see j of e^(S_j - lse).

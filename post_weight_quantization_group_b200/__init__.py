@@ -48,7 +48,7 @@ ABI_SYMBOLS = (
     "mxfp4_quantize", "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "q4_gemv_grouped",
     "fp4_gemm_workspace_bytes", "fp4_gemm", "bf16_ref_workspace_bytes",
     "kv_append_int8_paged", "kv_append_mass_int8_paged", "kv_gather_int8_paged", "kv_attention_workspace_bytes",
-    "kv_attention_int8_paged", "kv_attention_mass_int8_paged", "kv_evict_workspace_bytes",
+    "kv_attention_int8_paged", "kv_attention_fill_int8_paged", "kv_attention_mass_int8_paged", "kv_evict_workspace_bytes",
     "kv_evict_int8_paged",
 )
 
@@ -163,6 +163,7 @@ def load_library(path: str = LIB_PATH):
     lib.kv_attention_workspace_bytes.argtypes = [I32, I32, I32, I64]
     lib.kv_attention_workspace_bytes.restype = Z
     lib.kv_attention_int8_paged.argtypes = [KV, P, I64, I32, KB, F, I64, P, I64, P, P, Z, P]
+    lib.kv_attention_fill_int8_paged.argtypes = [*lib.kv_attention_int8_paged.argtypes[:-1], I32, P]
     lib.kv_attention_mass_int8_paged.argtypes = [KV, P, I64, I32, P, KB, F, I64, P, I64, P]
     lib.kv_evict_workspace_bytes.argtypes = [I32, I32, I64]
     lib.kv_evict_workspace_bytes.restype = Z
@@ -174,8 +175,8 @@ def load_library(path: str = LIB_PATH):
               "q8_quantize_per_channel", "q8_dequant", "q8_gemv", "kv_quantize_int8",
               "kv_dequant_int8", "kv_quantize_int4", "kv_dequant_int4", "mxfp4_quantize",
               "mxfp4_dequant", "nvfp4_quantize", "nvfp4_dequant", "fp4_gemm", "kv_append_int8_paged",
-              "kv_append_mass_int8_paged", "kv_gather_int8_paged", "kv_attention_int8_paged", "kv_attention_mass_int8_paged",
-              "kv_evict_int8_paged"):
+              "kv_append_mass_int8_paged", "kv_gather_int8_paged", "kv_attention_int8_paged",
+              "kv_attention_fill_int8_paged", "kv_attention_mass_int8_paged", "kv_evict_int8_paged"):
         getattr(lib, f).restype = S
     lib.q4_status_string.argtypes = [S]
     lib.q4_status_string.restype = ctypes.c_char_p
@@ -820,8 +821,9 @@ def kv_append_int8_paged(cache: KVPagedInt8, q: torch.Tensor | None, k: torch.Te
 
 def kv_gather_int8_paged(cache: KVPagedInt8, slots: torch.Tensor, k_out: torch.Tensor | None = None,
                          v_out: torch.Tensor | None = None, stream=None):
-    """(k, v) [tokens, heads, head_dim]: the dequantized rows of slots (rows of
-    negative slots are left as they are)."""
+    """(k, v) [tokens, heads, head_dim]: the dequantized rows of slots.  Rows of
+    negative slots are left as they are: in a k_out and v_out that this call
+    allocates they hold anything."""
     lib = load_library()
     cs = cache.c_struct()
     if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
@@ -851,7 +853,9 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     cu_new[b] .. cu_new[b + 1] - 1 of q; None: row b) over its seq_lens[b]
     cached tokens, the new ones among them; the last ``window`` of those a token
     sees, if given.  scale defaults to head_dim ** -0.5.  max_new: the most new
-    tokens of a sequence.  A workspace of your own has its first 256 KiB zero."""
+    tokens of a sequence.  A workspace of your own has its first 256 KiB zero.
+    Rows of q that no sequence names (a padded batch) are zeros and -inf in what
+    this call allocates, and left as they are in an out or lse of yours."""
     lib = load_library()
     cs = cache.c_struct()
     d, dt, tokens = cs.head_dim, cache.dtype, q.shape[0]
@@ -860,6 +864,9 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     batch = _kv_batch(block_table, seq_lens, cu_new, tokens, max_new)
     _own_workspace(workspace)
     _same_device(cache.k_codes, q, block_table, seq_lens, cu_new, out, lse, workspace)
+    fill = 0
+    if cu_new is not None or tokens > batch.seqs:  # else every row is named
+        fill = (1 if out is None else 0) | (2 if lse is None else 0)
     with _Call(q.device, stream) as call:
         if out is None:
             out = _empty_as(q)
@@ -871,10 +878,10 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
         if workspace is None:
             workspace = call.workspace(
                 _kv_workspace_bytes(q.device.index, d, hq, cs.heads, max(1, min(max_new, tokens))))
-        st = lib.kv_attention_int8_paged(
+        st = lib.kv_attention_fill_int8_paged(
             ctypes.byref(cs), q.data_ptr(), qs, hq, ctypes.byref(batch),
             d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), call.handle)
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), fill, call.handle)
     _check(st, "kv_attention_int8_paged")
     return out, lse
 

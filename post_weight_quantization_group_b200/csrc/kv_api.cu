@@ -343,9 +343,19 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
                                   int32_t q_heads, const kv_batch* batch, float scale,
                                   int64_t window, void* out, int64_t out_stride, float* lse,
                                   void* workspace, size_t workspace_bytes, q4_stream stream) {
+    return kv_attention_fill_int8_paged(cache, q, q_stride, q_heads, batch, scale, window, out, out_stride, lse,
+                                        workspace, workspace_bytes, 0, stream);
+}
+
+q4_status kv_attention_fill_int8_paged(const kv_paged_int8* cache, const void* q, int64_t q_stride,
+                                       int32_t q_heads, const kv_batch* batch, float scale,
+                                       int64_t window, void* out, int64_t out_stride, float* lse,
+                                       void* workspace, size_t workspace_bytes, int32_t fill,
+                                       q4_stream stream) {
     q4_status s = check_attention(cache, q, q_stride, q_heads, batch, scale, window);
     if (s != Q4_OK) return s;
-    if (batch->tokens == 0 || batch->seqs == 0) return Q4_OK;
+    if (fill < 0 || fill > 3) return Q4_ERR_INVALID_ARG;
+    if (batch->tokens == 0 || (batch->seqs == 0 && !fill)) return Q4_OK;
     const int64_t d = cache->head_dim;
     if ((s = check_rows(out, out_stride, q_heads * d)) != Q4_OK) return s;
     if (!aligned(lse, 4)) return Q4_ERR_ALIGNMENT;
@@ -368,12 +378,17 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
     a.out_stride = out_stride;
     a.q_heads = q_heads;
     a.scale_log2 = scale * 1.44269504f;
+    a.fill = fill;
     a.count = static_cast<unsigned*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsCounterBytes);
     a.status = q4_status_word();
     if (!a.status) return Q4_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = cache->dtype == Q4_BF16;
+    if (batch->seqs == 0) {  // nothing but rows to fill
+        const int64_t ctas = std::min<int64_t>(batch->tokens, sms);
+        return bf ? dispatch_rows<true, false>(a, 1, ctas, st) : dispatch_rows<false, false>(a, 1, ctas, st);
+    }
     if (p.tc && batch->tokens < max_new * batch->seqs) {
         // Chunks beside decode steps: those go to the other kernel, since a tile costs the
         // tensor-core kernel the same however few of its 256 rows are any (4 chunks of 257 and
@@ -387,6 +402,7 @@ q4_status kv_attention_int8_paged(const kv_paged_int8* cache, const void* q, int
         b.geom.lead = kKvLead;
         b.geom.rows_hi = 8 * few.nr;
         a.geom.rows_lo = 8 * few.nr;
+        a.fill = 0;
         s = bf ? dispatch_attention<true>(b, few, attn_grid(b, few.ctas), st)
                : dispatch_attention<false>(b, few, attn_grid(b, few.ctas), st);
         if (s != Q4_OK) return s;

@@ -66,6 +66,7 @@ struct KvAttn {
     float* part;       // partial slots, two per CTA: m [R], l [R], O [R, DP]
     unsigned* count;   // one per CTA
     unsigned* status;
+    int fill;  // of the rows that no sequence names: 1: zeros to out, 2: -inf to lse
 };
 
 constexpr int kKvWarps = 8;
@@ -159,6 +160,22 @@ __device__ __forceinline__ void kv_cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The rows of q that no sequence names, after kv_locate: before the first one's and behind
+// the last one's.
+template <int NT>
+__device__ __forceinline__ void kv_fill_unnamed(const KvAttn& a, const KvLocateShared& sh) {
+    if (!a.fill) return;
+    const int64_t lo = sh.named[0], hi = max(sh.named[1], lo);
+    for (int64_t u = blockIdx.x; u < a.batch.tokens - (hi - lo); u += gridDim.x) {
+        const int64_t row = u < lo ? u : u + (hi - lo);
+        if (a.fill & 1)
+            for (int i = threadIdx.x; i < a.q_heads * a.pool.d / 8; i += NT)
+                reinterpret_cast<uint4*>(a.out + row * a.out_stride)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if ((a.fill & 2) && a.lse)
+            for (int i = threadIdx.x; i < a.q_heads; i += NT) a.lse[row * a.q_heads + i] = -INFINITY;
+    }
+}
+
 // DP: head_dim padded to 64, 128 or 256.  NR: blocks of 8 rows (R = 8 NR).
 // MASS: not attention but the weight that each token receives, given the rows'
 // log-sum-exps: mass[j, h] += sum over the rows r that see j of exp(S[r, j] - lse_r).
@@ -194,6 +211,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, DP * NR > 128 ? 1 : 2)
     KvPlace w;
     kv_locate<kKvWarps * 32>(a.batch, a.geom, blockIdx.x, gridDim.x, 1, a.status, &s_loc, &T, &P,
                              &beg, &end, &w);
+    if constexpr (!MASS) kv_fill_unnamed<kKvWarps * 32>(a, s_loc);
     if (beg == end) return;
     KvSeq seq = kv_seq(a.batch, w.b, a.status);
     const int shift = (c.ps & (c.ps - 1)) == 0 ? 31 - __clz(c.ps) : -1;

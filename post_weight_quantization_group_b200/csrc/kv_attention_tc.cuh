@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
     KvPlace w;
     kv_locate<kTcaThreads>(a.batch, a.geom, blockIdx.x, gridDim.x, 1, a.status, &s_loc, &T, &P, &beg,
                            &end, &w);
+    kv_fill_unnamed<kTcaThreads>(a, s_loc);
     const int group = a.geom.group, window = a.geom.window;
     if (warp < 8) {
         // ------------------------------------------------------ softmax

@@ -437,7 +437,8 @@ __device__ __forceinline__ int64_t kv_block_scan(int64_t v, int64_t* sums, int64
 struct KvLocateShared {
     int64_t sums[32];
     KvPlace place;
-    int skip;  // empty places before the first tile
+    int skip;          // empty places before the first tile
+    int64_t named[2];  // rows of q [first, last) that the sequences name
 };
 template <int NT>
 __device__ __forceinline__ void kv_locate(const KvBatch& bt, const KvGeom& g, int64_t p, int64_t P,
@@ -445,11 +446,21 @@ __device__ __forceinline__ void kv_locate(const KvBatch& bt, const KvGeom& g, in
                                           int64_t* T, int64_t* Pused, int64_t* beg, int64_t* end,
                                           KvPlace* place) {
     int64_t all = 0, mine = 0, incl = 0;
+    if (bt.seqs == 0) {
+        if (threadIdx.x < 2) sh->named[threadIdx.x] = 0;
+        __syncthreads();
+    }
     // one pass when a block covers the sequences, else a pass for the total first
     const bool one = bt.seqs <= NT;
     for (int b0 = 0; b0 < bt.seqs; b0 += NT) {
         const int b = b0 + threadIdx.x;
-        mine = b < bt.seqs ? kv_seq_work(g, kv_seq(bt, b, status)) : 0;
+        mine = 0;
+        if (b < bt.seqs) {
+            const KvSeq s = kv_seq(bt, b, status);
+            mine = kv_seq_work(g, s);
+            if (b == 0) sh->named[0] = s.first;
+            if (b == bt.seqs - 1) sh->named[1] = s.first + s.n;
+        }
         int64_t t;
         incl = kv_block_scan<NT>(mine, sh->sums, &t);
         all += t;

@@ -1,0 +1,95 @@
+"""What a call of the paged INT8 cache returns and allocates by default."""
+import pytest
+import torch
+
+import post_weight_quantization_group_b200 as q4
+from test_gpu_kv_paged import BF, HF, _Case, _cuda32, _lib, _sync_ok  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _poison(*shapes):
+    """Leaves what is neither zero nor finite in the blocks that the next tensors get."""
+    keep = [torch.full(s, float("nan"), device="cuda") for s in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    del keep
+
+
+# sequences of (cached, new), rows of q behind the last one's
+UNNAMED = [([(40, 1), (300, 1)], 3), ([(500, 200)], 70), ([(90, 30), (700, 1), (0, 0)], 5), ([(20, 0)], 4)]
+
+
+@pytest.mark.parametrize("seqs,spare", UNNAMED)
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 2, 64), (4, 2, 256)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_rows_that_no_sequence_names(seqs, spare, hq, hk, d, dtype):
+    """A padded batch: zeros and -inf in what the call allocates, left as they
+    are in what it is given; the named rows are the same either way."""
+    c = _Case(seqs, hq, hk, d, 16, dtype, seed=3, spare_rows=spare)
+    o, l = torch.full(c.q.shape, 7.0, dtype=dtype, device="cuda"), torch.full(c.q.shape[:2], 5.0, device="cuda")
+    c.attention(out=o, lse=l)
+    _sync_ok()
+    assert torch.all(o[c.T:] == 7) and torch.all(l[c.T:] == 5)
+    rows = c.q.shape[0]
+    for kw in ({}, {"out": torch.full_like(o, 7.0)}, {"lse": torch.full_like(l, 5.0)}):
+        _poison((rows, hq, d // 2), (rows, hq))
+        got, lse = c.attention(**kw)
+        _sync_ok()
+        assert torch.equal(got[:c.T], o[:c.T]) and torch.equal(lse[:c.T], l[:c.T])
+        assert torch.all(got[c.T:] == (7 if "out" in kw else 0))
+        assert torch.all(lse[c.T:] == (5 if "lse" in kw else -float("inf")))
+
+
+def test_more_rows_than_sequences_without_cu_new():
+    c = _Case([(40, 1), (300, 1), (1, 1)], 8, 2, 128, 16, BF, seed=8, spare_rows=4)
+    want, wl = q4.kv_attention_int8_paged(c.cache, c.q[:3], c.table, c.len_t)
+    _poison((7, 8, 64), (7, 8))
+    got, lse = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t)
+    _sync_ok()
+    assert torch.equal(got[:3], want) and torch.equal(lse[:3], wl)
+    assert torch.all(got[3:] == 0) and torch.all(lse[3:] == -float("inf"))
+
+
+def test_rows_before_the_first_sequence_and_no_sequences():
+    c = _Case([(60, 5), (70, 2)], 8, 2, 128, 16, BF, seed=8, spare_rows=4)
+    want, wl = c.attention()
+    moved = torch.cat([c.q[-4:], c.q[:7]])
+    _poison((11, 8, 64), (11, 8))
+    got, lse = q4.kv_attention_int8_paged(c.cache, moved, c.table, c.len_t, c.cu_t + 4, max_new=5)
+    _sync_ok()
+    assert torch.equal(got[4:], want[:7]) and torch.equal(lse[4:], wl[:7])
+    assert torch.all(got[:4] == 0) and torch.all(lse[:4] == -float("inf"))
+    none = torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    _poison((11, 8, 64), (11, 8))
+    got, lse = q4.kv_attention_int8_paged(c.cache, moved, none, c.len_t[:0], c.cu_t[:1] * 0)
+    _sync_ok()
+    assert torch.all(got == 0) and torch.all(lse == -float("inf"))
+
+
+def test_unnamed_rows_of_a_captured_call():
+    """Replayed with fewer rows named than at the capture."""
+    c = _Case([(400, 60), (300, 1)], 8, 2, 128, 16, BF, seed=4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = c.attention()
+    for n in (60, 20, 41):
+        c.cu_t.copy_(_cuda32([0, n, n + 1]))
+        want, wl = c.attention()
+        out.fill_(9)
+        lse.fill_(9)
+        graph.replay()
+        _sync_ok()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert torch.all(out[n + 1:] == 0) and torch.all(lse[n + 1:] == -float("inf"))
+
+
+def test_the_default_stream_by_its_handle():
+    """stream=0 inside another stream's block."""
+    c = _Case([(400, 1), (300, 1)], 8, 2, 128, 16, BF, seed=4)
+    want, wl = c.attention()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got, lse = c.attention(stream=0)
+    torch.cuda.synchronize()
+    _sync_ok()
+    assert torch.equal(got, want) and torch.equal(lse, wl)

@@ -6,7 +6,7 @@ import pytest
 
 import post_weight_quantization_group_b200 as q4
 from post_weight_quantization_group_b200 import build as q4build
-from test_kv_paged_abi import A, POOL_FAULTS, _pool, _status
+from test_kv_paged_abi import A, BATCH_FAULTS, POOL_FAULTS, _batch, _pool, _status
 
 
 @pytest.fixture(scope="module")
@@ -33,3 +33,27 @@ def test_append_mass_faults(lib):
     assert _append_mass(lib, ms=31) == q4.Q4_ERR_SHAPE
     assert _append_mass(lib, mass=A + 2) == q4.Q4_ERR_ALIGNMENT
     assert _append_mass(lib, k=None) == q4.Q4_ERR_INVALID_ARG
+
+
+def _fill(lib, fill, pool=None, batch=None, **kw):
+    a = dict(out=A, ws=A, wsb=1 << 30)
+    a.update(kw)
+    return lib.kv_attention_fill_int8_paged(ctypes.byref(pool or _pool()), A, 256, 4, ctypes.byref(batch or _batch()),
+                                            1.0, 0, a["out"], 256, A, a["ws"], a["wsb"], fill, None)
+
+
+@pytest.mark.parametrize("kw,status", BATCH_FAULTS)
+def test_attention_fill_batch_faults(lib, kw, status):
+    assert _fill(lib, 3, batch=_batch(**kw)) == _status(status)
+
+
+def test_attention_fill_faults(lib):
+    for bad in (-1, 4, 1 << 20):
+        assert _fill(lib, bad) == q4.Q4_ERR_INVALID_ARG
+        assert _fill(lib, bad, batch=_batch(tokens=0)) == q4.Q4_ERR_INVALID_ARG
+    assert _fill(lib, 3, batch=_batch(tokens=0)) == q4.Q4_OK
+    assert _fill(lib, 0, batch=_batch(seqs=0)) == q4.Q4_OK
+    # rows to fill are an output even where there is no sequence
+    for seqs in (0, 3):
+        assert _fill(lib, 1, batch=_batch(seqs=seqs), out=None) == q4.Q4_ERR_INVALID_ARG
+        assert _fill(lib, 1, batch=_batch(seqs=seqs), ws=None) == q4.Q4_ERR_WORKSPACE
