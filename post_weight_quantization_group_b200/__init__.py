@@ -754,10 +754,12 @@ def _own_workspace(t: torch.Tensor | None):
         raise ValueError("workspace must be contiguous")
 
 
-def _kv_batch(block_table, seq_lens, cu_new, tokens: int, max_new: int) -> _CKVBatch:
+def _kv_batch(block_table, seq_lens, cu_new, tokens: int, max_new: int | None) -> _CKVBatch:
     if block_table.dim() != 2:
         raise ValueError("block_table must be [seqs, width]")
     seqs, width = block_table.shape
+    if max_new is None:  # the rows that are left where every other sequence has one
+        max_new = 1 if cu_new is None else max(tokens - seqs + 1, 1)
     _int32(block_table, "block_table", (seqs, width))
     _int32(seq_lens, "seq_lens", (seqs,))
     _int32(cu_new, "cu_new", (seqs + 1,))
@@ -846,14 +848,15 @@ def kv_gather_int8_paged(cache: KVPagedInt8, slots: torch.Tensor, k_out: torch.T
 
 def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: torch.Tensor,
                             seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
-                            max_new: int = 1, scale: float | None = None, window: int = 0,
+                            max_new: int | None = None, scale: float | None = None, window: int = 0,
                             out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                             workspace: torch.Tensor | None = None, stream=None):
     """(out, lse): causal attention of each sequence's new tokens (rows
     cu_new[b] .. cu_new[b + 1] - 1 of q; None: row b) over its seq_lens[b]
     cached tokens, the new ones among them; the last ``window`` of those a token
     sees, if given.  scale defaults to head_dim ** -0.5.  max_new: the most new
-    tokens of a sequence.  A workspace of your own has its first 256 KiB zero.
+    tokens of a sequence, by which the kernel is chosen; None: what the rows of q leave one
+    sequence where each of the others has one.  A workspace of your own has its first 256 KiB zero.
     Rows of q that no sequence names (a padded batch) are zeros and -inf in what
     this call allocates, and left as they are in an out or lse of yours."""
     lib = load_library()
@@ -875,9 +878,11 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
         elif lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous fp32 [tokens, q_heads]")
         os_ = _head_rows(out, "out", hq, d, dt, tokens)
+        need = _kv_workspace_bytes(q.device.index, d, hq, cs.heads, max(1, min(batch.max_new, tokens)))
         if workspace is None:
-            workspace = call.workspace(
-                _kv_workspace_bytes(q.device.index, d, hq, cs.heads, max(1, min(max_new, tokens))))
+            workspace = call.workspace(need)
+        elif max_new is None and workspace.numel() * workspace.element_size() < need:
+            batch.max_new = 1  # the kernel of few rows needs less
         st = lib.kv_attention_fill_int8_paged(
             ctypes.byref(cs), q.data_ptr(), qs, hq, ctypes.byref(batch),
             d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lse.data_ptr(),
@@ -889,7 +894,7 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
 def kv_attention_mass_int8_paged(cache: KVPagedInt8, q: torch.Tensor, lse: torch.Tensor,
                                  mass: torch.Tensor, block_table: torch.Tensor,
                                  seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
-                                 max_new: int = 1, scale: float | None = None, window: int = 0,
+                                 max_new: int | None = None, scale: float | None = None, window: int = 0,
                                  stream=None) -> torch.Tensor:
     """Adds to mass (fp32 [pages, heads, page_size]) the attention weight that
     each cached token received from these queries; lse as the attention call

@@ -83,6 +83,36 @@ def test_unnamed_rows_of_a_captured_call():
         assert torch.all(out[n + 1:] == 0) and torch.all(lse[n + 1:] == -float("inf"))
 
 
+@pytest.mark.parametrize("seqs", [[(600, 300)], [(500, 90), (40, 40), (77, 1)], [(50, 1), (60, 1)]])
+def test_max_new_from_the_rows(seqs):
+    """Without max_new the rows of q bound the new tokens, so a chunk gets the
+    chunks' kernel: bit for bit what the same bound gives when it is passed."""
+    c = _Case(seqs, 16, 2, 128, 16, BF, seed=6)
+    bound = max(c.T - len(seqs) + 1, 1)
+    want = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, max_new=bound)
+    got = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    m = [torch.zeros(c.cache.k_scales.shape, device="cuda") for _ in range(2)]
+    q4.kv_attention_mass_int8_paged(c.cache, c.q, want[1], m[0], c.table, c.len_t, c.cu_t, max_new=bound)
+    q4.kv_attention_mass_int8_paged(c.cache, c.q, want[1], m[1], c.table, c.len_t, c.cu_t)
+    _sync_ok()
+    assert torch.equal(*m)
+
+
+def test_max_new_from_the_rows_and_a_small_workspace():
+    """A workspace of the caller's that is enough for single tokens still serves."""
+    c = _Case([(600, 300)], 16, 2, 128, 16, BF, seed=6)
+    need = q4.load_library().kv_attention_workspace_bytes
+    assert need(128, 16, 2, 1) < need(128, 16, 2, 300)
+    want = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, max_new=1)
+    ws = torch.zeros(need(128, 16, 2, 1), dtype=torch.uint8, device="cuda")
+    got = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, workspace=ws)
+    _sync_ok()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(q4.Q4Error):
+        q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, max_new=300, workspace=ws)
+
+
 def test_the_default_stream_by_its_handle():
     """stream=0 inside another stream's block."""
     c = _Case([(400, 1), (300, 1)], 8, 2, 128, 16, BF, seed=4)
