@@ -691,7 +691,8 @@ Q4_API q4_status kv_attention_mass_int8_paged(const kv_paged_int8* cache, const 
  *             whole that way); or NULL or block_table itself: in place, where
  *             no page may belong to two of the sequences
  *   new_lens  int32 [seqs] (written): min(length, budget); may be seq_lens
- *   workspace kv_evict_workspace_bytes(seqs, heads, budget) bytes, 16-byte aligned
+ *   workspace kv_evict_workspace_bytes(seqs, heads, budget) bytes, 16-byte aligned;
+ *             4 * seqs where budget >= table_width * page_size (nothing can be over it)
  */
 Q4_API size_t kv_evict_workspace_bytes(int32_t seqs, int32_t heads, int64_t budget);
 Q4_API q4_status kv_evict_int8_paged(const kv_paged_int8* cache, float* mass, int64_t mass_stride,

@@ -949,7 +949,9 @@ def kv_evict_int8_paged(cache: KVPagedInt8, mass: torch.Tensor, block_table: tor
         if new_lens is None:
             new_lens = seq_lens.new_empty(seqs)
         if workspace is None:
-            need = int(lib.kv_evict_workspace_bytes(seqs, cs.heads, budget))
+            need = 4 * seqs  # where no sequence can be over the budget
+            if budget < batch.table_width * cs.page_size:
+                need = int(lib.kv_evict_workspace_bytes(seqs, cs.heads, budget))
             workspace = seq_lens.new_empty(need, dtype=torch.uint8)
         st = lib.kv_evict_int8_paged(
             ctypes.byref(cs), mass.data_ptr(), ms, ctypes.byref(batch), budget, recent, sinks,

@@ -515,9 +515,10 @@ q4_status kv_evict_int8_paged(const kv_paged_int8* cache, float* mass, int64_t m
     if (batch->seqs == 0) return Q4_OK;
     if (!mass || !new_lens) return Q4_ERR_INVALID_ARG;
     if (!aligned(mass, 4) || !aligned(new_lens, 4) || !aligned(dst_table, 4)) return Q4_ERR_ALIGNMENT;
-    if (!workspace ||
-        workspace_bytes < kv_evict_workspace_bytes(batch->seqs, cache->heads, budget))
-        return Q4_ERR_WORKSPACE;
+    // no sequence can be longer than cap: where that is within the budget nothing is selected
+    const size_t need = budget >= cap ? static_cast<size_t>(batch->seqs) * 4
+                                      : kv_evict_workspace_bytes(batch->seqs, cache->heads, budget);
+    if (!workspace || workspace_bytes < need) return Q4_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return Q4_ERR_ALIGNMENT;
     KvEvict a{};
     a.pool = pool_of(cache);

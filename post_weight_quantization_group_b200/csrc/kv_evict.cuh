@@ -20,7 +20,7 @@ struct KvEvict {
     int64_t mass_page;
     int budget, recent, sinks;
     int32_t* new_lens;  // [seqs]
-    int32_t* src;       // [seqs, heads, budget]: kept tokens in order
+    int32_t* src;       // [seqs, heads, budget]: kept tokens in order (none if budget >= batch.cap)
     int32_t* len;       // [seqs]: the lengths as the selection saw them
     unsigned* status;
 };

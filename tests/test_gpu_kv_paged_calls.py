@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import post_weight_quantization_group_b200 as q4
-from test_gpu_kv_paged import BF, HF, _Case, _cuda32, _lib, _sync_ok  # noqa: F401
+from test_gpu_kv_paged import BF, HF, _Case, _cuda32, _gen, _lib, _pool, _sync_ok  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -111,6 +111,40 @@ def test_max_new_from_the_rows_and_a_small_workspace():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(q4.Q4Error):
         q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, max_new=300, workspace=ws)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("budget", [128, 1 << 20, 1 << 30])
+def test_evict_to_more_than_the_tables_name(budget, in_place):
+    """A budget that no sequence can pass moves nothing away, and asks for no
+    workspace beyond the lengths."""
+    lens = [100, 0, 33]
+    cache = _pool(40, 2, 16, 64, BF, 5)
+    mass = torch.rand(40, 2, 16, generator=_gen(1), device="cuda")
+    table = _cuda32([list(range(8)), list(range(8, 16)), list(range(16, 24))])
+    dst = None if in_place else _cuda32([list(range(24, 31)) + [-1], [-1] * 8, [31, 32, 33] + [-1] * 5])
+    before = [x.clone() for x in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, mass)]
+    len_t = _cuda32(lens)
+    torch.cuda.synchronize()
+    base = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    got = q4.kv_evict_int8_paged(cache, mass, table, len_t, budget, recent=4, sinks=2, dst_table=dst)
+    assert torch.cuda.max_memory_allocated() - base <= 8192
+    assert q4.q4_sync_status() == q4.Q4_OK and got.tolist() == lens
+    for x, y in zip((cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, mass), before):
+        if in_place:
+            assert torch.equal(x, y)
+        else:
+            want = y.clone()
+            for b, row in ((0, range(24, 31)), (2, range(31, 34))):
+                for i in range(lens[b]):
+                    want[row[i // 16], :, i % 16] = y[8 * b + i // 16, :, i % 16]
+            assert torch.equal(x, want)
+    ws = torch.zeros(12, dtype=torch.uint8, device="cuda")
+    got = q4.kv_evict_int8_paged(cache, mass, table, len_t, budget, dst_table=dst, workspace=ws)
+    assert q4.q4_sync_status() == q4.Q4_OK and got.tolist() == lens
+    with pytest.raises(q4.Q4Error):
+        q4.kv_evict_int8_paged(cache, mass, table, len_t, budget, dst_table=dst, workspace=ws[:8])
 
 
 def test_the_default_stream_by_its_handle():

@@ -57,3 +57,15 @@ def test_attention_fill_faults(lib):
     for seqs in (0, 3):
         assert _fill(lib, 1, batch=_batch(seqs=seqs), out=None) == q4.Q4_ERR_INVALID_ARG
         assert _fill(lib, 1, batch=_batch(seqs=seqs), ws=None) == q4.Q4_ERR_WORKSPACE
+
+
+def test_evict_workspace(lib):
+    """Enough for the selection, or for the lengths alone where the tables (4 pages of 16) name
+    no more than the budget."""
+    def call(budget, wsb):
+        return lib.kv_evict_int8_paged(ctypes.byref(_pool()), A, 32, ctypes.byref(_batch()), budget, 1, 1, None, 0, A,
+                                       A, wsb, None)
+
+    assert call(63, lib.kv_evict_workspace_bytes(3, 2, 63) - 1) == q4.Q4_ERR_WORKSPACE
+    for budget in (64, 65, 1 << 30):
+        assert call(budget, 11) == q4.Q4_ERR_WORKSPACE
