@@ -677,6 +677,13 @@ def _same_device(first: torch.Tensor, *rest):
             raise ValueError("all tensors of a call must be on one device")
 
 
+def _same_stream_device(device: torch.device, stream):
+    """A stream of another device is refused: the kernel would run there, on
+    this device's addresses.  (A bare handle does not tell its device.)"""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+
+
 class _Call:
     """The device and stream of a call whose tensors are on ``device``: the
     stream given, or that device's current one.  Inside the ``with`` block the
@@ -684,6 +691,7 @@ class _Call:
     call allocates belongs to the stream that uses it."""
 
     def __init__(self, device: torch.device, stream):
+        _same_stream_device(device, stream)
         self.device = device
         current = torch._C._cuda_getCurrentRawStream(device.index)
         self.handle = current if stream is None else _stream(stream)

@@ -3,6 +3,7 @@ No GPU needed; every call here is refused or has nothing to do."""
 import ctypes
 
 import pytest
+import torch
 
 import post_weight_quantization_group_b200 as q4
 from post_weight_quantization_group_b200 import build as q4build
@@ -69,3 +70,16 @@ def test_evict_workspace(lib):
     assert call(63, lib.kv_evict_workspace_bytes(3, 2, 63) - 1) == q4.Q4_ERR_WORKSPACE
     for budget in (64, 65, 1 << 30):
         assert call(budget, 11) == q4.Q4_ERR_WORKSPACE
+
+
+def test_a_stream_of_another_device(monkeypatch):
+    class Stream:  # as much of a torch stream as is looked at
+        def __init__(self, device):
+            self.device, self.cuda_stream = torch.device(device), 0x1234
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(ValueError):
+        q4._Call(torch.device("cuda", 0), Stream("cuda:1"))
+    q4._same_stream_device(torch.device("cuda", 0), Stream("cuda:0"))
+    q4._same_stream_device(torch.device("cuda", 0), None)
+    q4._same_stream_device(torch.device("cuda", 0), 0x1234)
