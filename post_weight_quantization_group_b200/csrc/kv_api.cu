@@ -190,7 +190,7 @@ q4_status run_mass_tc(const KvMassTc& a, int64_t grid, cudaStream_t st) {
 // Chunks with head_dim above 128.
 template <bool BF16>
 q4_status run_mass(const KvMass& a, int64_t grid, cudaStream_t st) {
-    return launch_ex(kv_mass_kernel<BF16, 256>, dim3(static_cast<unsigned>(grid)), dim3(kKvWarps * 32), 0,
+    return launch_ex(kv_mass_kernel<BF16>, dim3(static_cast<unsigned>(grid)), dim3(kKvWarps * 32), 0,
                      1, true, st, a);
 }
 

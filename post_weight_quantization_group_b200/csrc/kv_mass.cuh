@@ -1,4 +1,6 @@
-// kv_mass.cuh -- the attention weight that cached tokens received,
+// kv_mass.cuh -- the attention weight that cached tokens received from chunks
+// of new tokens, for head_dim above 128 (below: kv_mass_tc.cuh; decode steps:
+// kv_attention.cuh),
 //   mass[j, h] += sum over the new tokens' rows r of KV head h that see j
 //                 of exp(scale (q_r . kq_j) sk_j - lse_r),
 // lse_r being the log-sum-exp that the attention call returned for the row.
@@ -6,8 +8,7 @@
 // The keys stay and the rows go by: a warp holds 16 tokens' K codes as the A
 // fragments of S^T = K q^T (mma.sync m16n8k16) and walks over the rows that see
 // any of its tokens, so a key's sum is a thread's own and needs no partial
-// results.  For decode steps (8 rows) it reads K once and is bound by HBM; for
-// chunks it is bound by the exponentials and the MMAs.  The result is added
+// results.  Every warp reads the rows for itself, through L2.  The result is added
 // with one atomic per token and head: a slot that one sequence names gets one
 // addend (any order gives the same sum); a page that several sequences share
 // gets all of theirs.
@@ -44,9 +45,9 @@ __device__ __forceinline__ int kv_mass_tiles(const KvMass& a, const KvSeq& s, in
     return max((s.len + kKvTile - 1) / kKvTile - *lo, 0);
 }
 
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(kKvWarps * 32, DP == 256 ? 1 : 2)
-    kv_mass_kernel(const __grid_constant__ KvMass a) {
+template <bool BF16>
+__global__ void __launch_bounds__(kKvWarps * 32, 1) kv_mass_kernel(const __grid_constant__ KvMass a) {
+    constexpr int DP = 256;  // head_dim, padded
     constexpr int U = DP / 64;
     constexpr int NT = kKvWarps * 32;
     __shared__ int64_t s_sums[32];

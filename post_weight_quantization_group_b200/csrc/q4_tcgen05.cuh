@@ -89,12 +89,6 @@ __device__ __forceinline__ void tmem_st_frag16w(uint32_t taddr, const uint32_t* 
 }
 // Sixteen lanes x 8 columns of packed pairs in the same layout: v[2 i] is column
 // 4 i + lane % 4 of lane lane / 4, v[2 i + 1] of lane lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_pairs8(uint32_t taddr, uint32_t* v) {
-    asm volatile("tcgen05.ld.sync.aligned.16x128b.x2.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(taddr)
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_st_pairs8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3])
