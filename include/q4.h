@@ -551,7 +551,8 @@ typedef struct kv_batch {
                                    b's new tokens, its last ones; NULL: row b is sequence b's one
                                    new token */
     int64_t table_width;        /* table_width * page_size <= 2^30 */
-    int64_t tokens;             /* rows of q; rows that no sequence names are left as they are */
+    int64_t tokens;             /* rows of q; rows that no sequence names are left as they are (or
+                                   filled: kv_attention_fill_int8_paged) */
     int64_t max_new;            /* >= 1: the most new tokens of a sequence.  Only the choice of
                                    kernel depends on it. */
     int32_t seqs;
@@ -625,7 +626,8 @@ Q4_API q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t*
  * gives zeros and lse = -inf.  q_heads is a multiple of the cache's heads:
  * query head h reads KV head h / (q_heads / heads).  The softmax is in fp32
  * with one rounding of the weights before the product with V: of weight times
- * V scale to fp16 (2^-11), or to 2^-32 of the row's largest where that is more.
+ * V scale to fp16 (2^-11), or to 2^-32 of the row's largest where that is more
+ * (chunks: two, of some weights of a 128-token tile in which the row's maximum grows).
  * V scales below 2^-80 count as 2^-80.  Sums are in fp32: one over n tokens may lose
  * n * 2^-23 of itself.  A masked token's row does not reach
  * the output whatever its scales hold; a visible NaN does.

@@ -328,9 +328,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1)
                 // p' = 2^(x - m) with the m' known so far, their sum with 1 / sv into l. The
                 // packed p' of columns 16 q .. go over columns 8 q .. of S, which have been read.
                 // Columns whose maximum is more than kKvTop above m (rare after a segment's
-                // first tile) raise m first and rescale what has been added with the old one by a
-                // power of two: l, O and this tile's earlier weights (a second rounding for those
-                // that it takes below fp16's normals).
+                // first tile) raise m first and rescale what has been added with the old one:
+                // l, O and this tile's earlier weights (a second rounding to fp16 for those).
                 uint64_t lx[4], neg_m[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -1,7 +1,12 @@
 """The paged INT8 cache's attention and mass where a CTA has much to do: many
 tiles of a unit one after another, many units, against the fp64 definition.  What a
 CTA gets is computed with a model of the division of work, so that the
-cases keep reaching what they are for."""
+cases keep reaching what they are for.
+
+Bounds as in test_gpu_kv_paged.py, with the terms of test_gpu_kv_paged_weights.py for weights
+that are far below a row's largest and, in chunks, are rounded twice; the accumulators' own term
+is left out, which is stricter.
+"""
 import numpy as np
 import pytest
 import torch
@@ -41,13 +46,13 @@ def _sms():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
 
-def _check(c, window=0):
+def _check(c, window=0, chunk=False):
     scale = c.d ** -0.5
     out, lse = c.attention(window=window)
     _sync_ok()
     o, l, spread, floor, reach = dense.attention(c.cache, c.q, c.rows, c.lens, c.cu, c.ps, scale, window)
     ds = _d_s(reach)
-    bound = torch.finfo(c.dtype).eps / 2 * o.abs() + spread * (2.0 ** -11 + 4 * ds[..., None]) \
+    bound = torch.finfo(c.dtype).eps / 2 * o.abs() + spread * ((2.0 ** -10 if chunk else 2.0 ** -11) + 4 * ds[..., None]) \
         + 1.01 * 2.0 ** -32 * floor + torch.finfo(c.dtype).tiny
     err = (out.double() - o).abs()
     assert bool((err <= bound).all()), f"out: worst {float((err / bound).max()):.3f}"
@@ -91,7 +96,7 @@ def test_chunk_many_tiles(hq, hk, d, ps, dtype, seqs, window, rising):
     c = _Case(seqs, hq, hk, d, ps, dtype, seed=d)
     most, _ = _reached(c, 256, 1, _sms(), window)
     assert most >= 10
-    _check(_rising(c) if rising else c, window)
+    _check(_rising(c) if rising else c, window, chunk=True)
 
 
 @pytest.mark.parametrize("d,dtype", [(128, BF), (96, HF), (64, BF), (16, HF)])
@@ -102,7 +107,7 @@ def test_chunk_many_segments(d, dtype):
     c = _Case(seqs, 16, 2, d, 16, dtype, seed=d)
     most, segs = _reached(c, 256, 1, _sms())
     assert segs > 5
-    _check(c)
+    _check(c, chunk=True)
 
 
 @pytest.mark.parametrize("d,dtype", [(128, HF), (64, BF), (256, BF)])

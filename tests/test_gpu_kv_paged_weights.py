@@ -4,15 +4,16 @@ tokens far above all the others of a long context.
 Bounds as in test_gpu_kv_paged.py, with two more terms and a third made tighter.
   Weights below fp16's normals.  A row's weights are rounded to fp16 on a scale where its
   largest (weight times V scale) lies at 2^7 or above, so a weight is off by 2^-11 of itself
-  or by 2^-25 on that scale, 2^-32 of the largest.  A weight that a growing maximum has moved is
-  rounded once more, by as much again times the factor of the move (2^-8 at most).
+  or by 2^-25 on that scale, 2^-32 of the largest.  In a tile of a chunk in which a row's maximum
+  grows, the weights before it are rounded a second time, after a factor of 2^-8 or less: another 2^-11 of
+  themselves, and 2^-25 of which the first one's is 2^-8.
   Accumulators.  An fp32 accumulator of the tensor cores that holds A adds a product aligned to
   A's exponent and cuts what lies below its last place: each is off by less than 2^-23 |A|,
   |A| <= sum p|v|.  It adds all n tokens of a row in the kernel of chunks, an eighth of them (one
   warp's) in that of single tokens.
   The weights' sum is rounded to nearest, 2^-24 of it at each addition: a thread makes n / 8 (chunks: 16
   packed pairs of a tile's 128) or n / 64 of them.
-  out       e |ref| + sum p|v| (2^-11 + 4 dS + adds 2^-23) + 1.01 2^-32 max(p sv) sum |vq|
+  out       e |ref| + sum p|v| (2^-11 + 4 dS + adds 2^-23) + 1.01 2^-32 max(p sv) sum |vq|; chunks: 2^-10
   lse       2 dS + 2^-22 |lse| + adds 2^-24
 """
 import math
@@ -32,7 +33,8 @@ def _check(cache, q, table, lens, cu, ps, scale, got, chunk, what=""):
     o, l, spread, floor, reach = dense.attention(cache, q, table, lens, cu, ps, scale)
     ds, n = _d_s(reach), max(lens)
     fi = torch.finfo(q.dtype)
-    bound = fi.eps / 2 * o.abs() + spread * (2.0 ** -11 + 4 * ds[..., None] + (n if chunk else n / 8) * 2.0 ** -23) \
+    bound = fi.eps / 2 * o.abs() + spread * ((2.0 ** -10 if chunk else 2.0 ** -11) + 4 * ds[..., None] +
+                                             (n if chunk else n / 8) * 2.0 ** -23) \
         + 1.01 * 2.0 ** -32 * floor + fi.tiny * fi.eps
     err = (out.double() - o).abs()
     assert bool((err <= bound).all()), f"{what} out: worst {float((err / bound).max()):.3f}"
