@@ -628,7 +628,8 @@ Q4_API q4_status kv_gather_int8_paged(const kv_paged_int8* cache, const int64_t*
  * with one rounding of the weights before the product with V: of weight times
  * V scale to fp16 (2^-11), or to 2^-32 of the row's largest where that is more
  * (chunks: two, of some weights of a 128-token tile in which the row's maximum grows).
- * V scales below 2^-80 count as 2^-80.  Sums are in fp32: one over n tokens may lose
+ * V scales below 2^-80 count as 2^-80, and tokens whose weight times V scale is below
+ * 2^-133 of the row's largest count as nothing.  Sums are in fp32: one over n tokens may lose
  * n * 2^-23 of itself.  A masked token's row does not reach
  * the output whatever its scales hold; a visible NaN does.
  *   q          [tokens, q_heads, head_dim] in the cache type, rows q_stride apart

@@ -165,11 +165,12 @@ __device__ __forceinline__ void kv_cp_wait() {
 template <int NT>
 __device__ __forceinline__ void kv_fill_unnamed(const KvAttn& a, const KvLocateShared& sh) {
     if (!a.fill) return;
+    const int64_t chunks = static_cast<int64_t>(a.q_heads) * a.pool.d / 8;  // of 16 bytes
     const int64_t lo = sh.named[0], hi = max(sh.named[1], lo);
     for (int64_t u = blockIdx.x; u < a.batch.tokens - (hi - lo); u += gridDim.x) {
         const int64_t row = u < lo ? u : u + (hi - lo);
         if (a.fill & 1)
-            for (int i = threadIdx.x; i < a.q_heads * a.pool.d / 8; i += NT)
+            for (int64_t i = threadIdx.x; i < chunks; i += NT)
                 reinterpret_cast<uint4*>(a.out + row * a.out_stride)[i] = make_uint4(0u, 0u, 0u, 0u);
         if ((a.fill & 2) && a.lse)
             for (int i = threadIdx.x; i < a.q_heads; i += NT) a.lse[row * a.q_heads + i] = -INFINITY;
