@@ -11,8 +11,9 @@
 // memory; it is rescaled only when a row's x passes its m' by more than kKvTop.
 //
 // Measured (B200): 1024 new tokens over 32,768, 64 query heads over 8 of 128,
-// 1.66 ms = 657 TFLOP/s; bound by the latency of the softmax warps' instructions
-// (a pass takes 3600 cycles beside 2050 of MMA).
+// 1.68 ms = 650 TFLOP/s.  A tile takes 6050 cycles, of which its products need 2050: a
+// softmax warp works 3600 and waits 1800 to 2100 for its half's next scores, which
+// wait for the P V before them (P lies over S).
 //
 //   warps 0-3 / 4-7   softmax of half A / B
 //   warps 8-11        conversion: codes from the pages (16-byte loads, a tile

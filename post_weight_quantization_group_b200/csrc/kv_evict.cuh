@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(256) kv_evict_copy_kernel(const __grid_constan
 // one), so rows moved in order, a block of 256 read before any of it is
 // written, overwrite nothing that is still to be read.  The order binds only
 // rows of the same bytes: a CTA takes one (sequence, head) and one 32-byte
-// column of the K or the V codes, or the scales and mass (blockIdx.x).
+// column of the K or the V codes, or the scales and mass (blockIdx.x).  With the
+// selection, 8 heads of 32,768 tokens to 4096: 40 us (into other pages 19).
 __global__ void __launch_bounds__(256) kv_evict_inplace_kernel(const __grid_constant__ KvEvict a) {
     grid_launch_dependents();
     grid_dependency_wait();

@@ -8,7 +8,8 @@
 // The keys stay and the rows go by: a warp holds 16 tokens' K codes as the A
 // fragments of S^T = K q^T (mma.sync m16n8k16) and walks over the rows that see
 // any of its tokens, so a key's sum is a thread's own and needs no partial
-// results.  Every warp reads the rows for itself, through L2.  The result is added
+// results.  Every warp reads the rows for itself, through L2 (256 new tokens over 8192,
+// 16/8 heads of 256: 346 us).  The result is added
 // with one atomic per token and head: a slot that one sequence names gets one
 // addend (any order gives the same sum); a page that several sequences share
 // gets all of theirs.

@@ -144,7 +144,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 //   within 2e-7 of a turn), then sine and cosine of the remainder in fp32.
 // K is quantized from its fp32 rotated value: a rounding to the cache type in
 // between would add an error of its own.  Every element is read and written
-// once; bound by the instruction rate (0.71 of the issue slots), so a warp
+// once; the instruction rate is its nearest bound (0.71 of the issue slots, half of HBM's rate), so a warp
 // whose heads are all queries has a path of its own, without the quantization
 // and without branches (8191 tokens of 64/8 heads of 128: 98 us, 3.1 TB/s; with
 // branches and one path 130; three heads under way instead of one 98; the
