@@ -762,12 +762,22 @@ def _own_workspace(t: torch.Tensor | None):
         raise ValueError("workspace must be contiguous")
 
 
+def _likely_max_new(tokens: int, seqs: int) -> int:
+    """The most new tokens of a sequence, as far as the numbers of rows and sequences
+    tell: the same for each where they divide evenly (prompts of one length, drafts),
+    else the rows that are left where each of the others has one (a chunk beside
+    decode steps)."""
+    if seqs > 0 and tokens % seqs == 0:
+        return max(tokens // seqs, 1)
+    return max(tokens - max(seqs, 1) + 1, 1)
+
+
 def _kv_batch(block_table, seq_lens, cu_new, tokens: int, max_new: int | None) -> _CKVBatch:
     if block_table.dim() != 2:
         raise ValueError("block_table must be [seqs, width]")
     seqs, width = block_table.shape
-    if max_new is None:  # the rows that are left where every other sequence has one
-        max_new = 1 if cu_new is None else max(tokens - seqs + 1, 1)
+    if max_new is None:
+        max_new = _likely_max_new(tokens, seqs) if cu_new is not None else 1
     _int32(block_table, "block_table", (seqs, width))
     _int32(seq_lens, "seq_lens", (seqs,))
     _int32(cu_new, "cu_new", (seqs + 1,))
@@ -863,8 +873,8 @@ def kv_attention_int8_paged(cache: KVPagedInt8, q: torch.Tensor, block_table: to
     cu_new[b] .. cu_new[b + 1] - 1 of q; None: row b) over its seq_lens[b]
     cached tokens, the new ones among them; the last ``window`` of those a token
     sees, if given.  scale defaults to head_dim ** -0.5.  max_new: the most new
-    tokens of a sequence, by which the kernel is chosen; None: what the rows of q leave one
-    sequence where each of the others has one.  A workspace of your own has its first 256 KiB zero.
+    tokens of a sequence, by which the kernel is chosen; None: a guess from the numbers of
+    rows and sequences.  A workspace of your own has its first 256 KiB zero.
     Rows of q that no sequence names (a padded batch) are zeros and -inf in what
     this call allocates, and left as they are in an out or lse of yours."""
     lib = load_library()

@@ -83,12 +83,12 @@ def test_unnamed_rows_of_a_captured_call():
         assert torch.all(out[n + 1:] == 0) and torch.all(lse[n + 1:] == -float("inf"))
 
 
-@pytest.mark.parametrize("seqs", [[(600, 300)], [(500, 90), (40, 40), (77, 1)], [(50, 1), (60, 1)]])
-def test_max_new_from_the_rows(seqs):
-    """Without max_new the rows of q bound the new tokens, so a chunk gets the
-    chunks' kernel: bit for bit what the same bound gives when it is passed."""
+@pytest.mark.parametrize("seqs,bound", [([(600, 300)], 300), ([(500, 90), (40, 40), (77, 1)], 129),
+                                        ([(50, 1), (60, 1)], 1), ([(400, 2), (9, 2), (70, 2)], 2)])
+def test_max_new_from_the_rows(seqs, bound):
+    """Without max_new it is guessed from the rows of q, so a chunk gets the
+    chunks' kernel: bit for bit what the same number gives when it is passed."""
     c = _Case(seqs, 16, 2, 128, 16, BF, seed=6)
-    bound = max(c.T - len(seqs) + 1, 1)
     want = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t, max_new=bound)
     got = q4.kv_attention_int8_paged(c.cache, c.q, c.table, c.len_t, c.cu_t)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

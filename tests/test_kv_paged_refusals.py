@@ -1,5 +1,6 @@
-"""Refusals of the paged INT8 KV-cache calls on the host, before any CUDA call.
-No GPU needed; every call here is refused or has nothing to do."""
+"""Refusals of the paged INT8 KV-cache calls on the host, before any CUDA call, and
+the binding's guess of the new tokens.  No GPU needed; every call here is refused or
+has nothing to do."""
 import ctypes
 
 import pytest
@@ -83,3 +84,10 @@ def test_a_stream_of_another_device(monkeypatch):
     q4._same_stream_device(torch.device("cuda", 0), Stream("cuda:0"))
     q4._same_stream_device(torch.device("cuda", 0), None)
     q4._same_stream_device(torch.device("cuda", 0), 0x1234)
+
+
+def test_likely_max_new():
+    guess = q4._likely_max_new
+    assert guess(300, 1) == 300 and guess(64, 64) == 1 and guess(64, 32) == 2  # a prompt, decode steps, drafts
+    assert guess(363, 64) == 300  # a chunk of 300 beside 63 decode steps
+    assert guess(0, 5) == 1 and guess(3, 5) == 1 and guess(7, 0) == 7
